@@ -56,8 +56,9 @@
  *             arguments are valid but the library has no kernel for the
  *             shape or dtype combination; there is no fallback path.
  *   Aliasing: outputs must not overlap inputs, except that
- *             retention_recurrent_step(s) update `state` in place by design
- *             and retention_rope may rotate q and k in place.
+ *             retention_recurrent_step(s) update `state` in place by design,
+ *             retention_rope may rotate q and k in place and
+ *             retention_glr_step may write the state over itself.
  */
 #ifndef RETENTION_H_
 #define RETENTION_H_
@@ -489,6 +490,156 @@ RET_API ret_status retention_chunkwise_fwd_rope(const void* q, const void* k, co
 RET_API ret_status msr_norm_gate(const void* o, ret_dtype o_dtype, const ret_norm_gate* ng,
                          void* y, ret_dtype y_dtype, int ntok, int H, int dv,
                          ret_stream_t stream);
+
+/*
+ * Gated linear recurrence (ql.gl blog on Griffin/Hawk, section "Hawk":
+ * h_t = a_t . h_(t-1) + b_t . x_t element by element, the gates computed from
+ * the token).  The page gives no formula for the gates; the form taken is a
+ * decay that depends on the token through a sigmoid and an input gate scaled so
+ * that the state keeps unit variance.  For each channel, with the projected
+ * gate inputs r_t, i_t and a learned parameter lam:
+ *     s_t = sigmoid(r_t),  y_t = c softplus(lam) s_t,  a_t = exp(-y_t)
+ *     b_t = sqrt(1 - a_t^2) sigmoid(i_t)
+ *     h_t = a_t h_(t-1) + b_t x_t
+ * The recurrent state is one float32 vector per sequence: [nseq|B, D].
+ *   x, r, i: [B,T,D] in_dtype (packed: B = 1 with cu_seqlens/nseq as for
+ *   retention_chunkwise_fwd; every sequence starts from its own state)
+ *   lam: [D] float32 device      c: finite, > 0
+ *   state_in, state_out: [nseq|B, D] float32 or NULL (zeros / not emitted); an
+ *          empty sequence's state_out equals its state_in.
+ *   h: [B,T,D] h_dtype, written in full
+ *   chunk_states: NULL, or [retention_glr_chunk_slots(...), D] float32: the
+ *          state entering every RETENTION_GLR_CHUNK tokens of each sequence,
+ *          which is all that retention_glr_bwd needs of the forward.  The
+ *          chunks of sequence s, which starts at flat token n, are the rows
+ *          n / RETENTION_GLR_CHUNK + s, and on; rows between two sequences may
+ *          stay unwritten.
+ * All arithmetic is float32, whatever the inputs' type; h is rounded once when
+ * it is stored as bf16.  1 - a^2 is formed without cancellation for decays near
+ * one.  No workspace.  Inconsistent cu_seqlens are clamped and reported as
+ * RET_ERR_DEVICE_DATA.
+ * Supported: any T (packed T = 0 included) with B*T < 2^31, D in 1..2^20;
+ * element offsets are 64-bit.
+ */
+#define RETENTION_GLR_CHUNK 64
+
+RET_API size_t retention_glr_chunk_slots(int B, int T, int nseq);
+RET_API ret_status retention_glr_fwd(const void* x, const void* r, const void* i,
+                                     ret_dtype in_dtype, const float* lam, double c,
+                                     const int32_t* cu_seqlens, int nseq, const float* state_in,
+                                     float* state_out, void* h, ret_dtype h_dtype,
+                                     float* chunk_states, int B, int T, int D,
+                                     ret_stream_t stream);
+
+/*
+ * Gradients of retention_glr_fwd.  With upstream gradients dH = d_h and dS =
+ * d_state_out (zero if NULL), per sequence of T tokens and e_(T+1) = dS:
+ *     G_t = dH_t + e_(t+1),   e_t = a_t G_t,   d_state_in = e_1
+ *     dx_t = G_t b_t          di_t = G_t b_t x_t (1 - sigmoid(i_t))
+ *     u_t  = G_t (y_t a_t^2 sigmoid(i_t) x_t / sqrt(1 - a_t^2) - a_t y_t h_(t-1))
+ *     dr_t = u_t (1 - s_t)    d_lam = sum_t u_t sigmoid(lam) / softplus(lam)
+ * The h_(t-1) are formed again in float32 from chunk_states, so neither h nor
+ * state_in is read.  At a_t = 1 (where the derivative of the square root has a
+ * pole that y_t cancels) the y_t / sqrt(1 - a_t^2) term is its limit, zero.
+ *   x, r, i, lam, c, cu_seqlens, nseq: as given to the forward
+ *   chunk_states: as the forward wrote them
+ *   d_h: [B,T,D] dh_dtype        d_state_out: [nseq|B, D] float32 or NULL
+ *   dx, dr, di: [B,T,D] grad_dtype, written in full
+ *   d_lam: [D] float32           d_state_in: [nseq|B, D] float32 or NULL
+ *   workspace: at least retention_glr_bwd_workspace_size(...) bytes, 256-byte
+ *          aligned (partial sums of d_lam, added in a fixed order: results are
+ *          the same from run to run)
+ * Supported: as retention_glr_fwd.
+ */
+RET_API size_t retention_glr_bwd_workspace_size(int B, int T, int D, int nseq);
+RET_API ret_status retention_glr_bwd(const void* x, const void* r, const void* i,
+                                     ret_dtype in_dtype, const float* lam, double c,
+                                     const int32_t* cu_seqlens, int nseq,
+                                     const float* chunk_states, const void* d_h,
+                                     ret_dtype dh_dtype, const float* d_state_out, void* dx,
+                                     void* dr, void* di, ret_dtype grad_dtype, float* d_lam,
+                                     float* d_state_in, void* workspace, size_t workspace_bytes,
+                                     int B, int T, int D, ret_stream_t stream);
+
+/*
+ * One token of the gated linear recurrence for N independent sequences (the
+ * decode step beside retention_recurrent_step):
+ *     state_out <- a state + b x,   h = state_out
+ *   x, r, i: [N,D] in_dtype     state, state_out: [N,D] float32; state_out may
+ *   equal state (in place)      h: [N,D] h_dtype, or NULL (not emitted)
+ * Supported: N >= 1, D in 1..2^20; element offsets are 64-bit.
+ */
+RET_API ret_status retention_glr_step(const void* x, const void* r, const void* i,
+                                      ret_dtype in_dtype, const float* lam, double c,
+                                      const float* state, float* state_out, void* h,
+                                      ret_dtype h_dtype, int N, int D, ret_stream_t stream);
+
+/*
+ * Layer norm over the last dimension, the pre-norm of a retention block
+ * (abeam.tech summary, 「技術の仕組み」: the block is residual, layer norm,
+ * retention and feed-forward).  For each token, over its D channels:
+ *     mu = mean x,  var = mean (x - mu)^2 (biased),  rstd = 1 / sqrt(var + eps)
+ *     y = (x - mu) rstd weight + bias
+ *   x: [ntok,D] x_dtype      y: [ntok,D] y_dtype (may not alias x)
+ *   weight, bias: [D] float32, or NULL for 1 and 0
+ *   mean, rstd: [ntok] float32, or NULL (not emitted); retention_layer_norm_bwd
+ *          reads them
+ * The statistics are float32 and the variance is taken about the mean (two
+ * passes over the row, which stays in registers).
+ * Supported: ntok >= 0 (0 enqueues nothing), D in 1..16384, eps >= 0 and
+ * finite; element offsets are 64-bit.
+ */
+RET_API ret_status retention_layer_norm_fwd(const void* x, ret_dtype x_dtype, const float* weight,
+                                            const float* bias, double eps, void* y,
+                                            ret_dtype y_dtype, float* mean, float* rstd, int ntok,
+                                            int D, ret_stream_t stream);
+
+/*
+ * Gradients of the layer norm.  With xh = (x - mean) rstd and n = d_y weight:
+ *     dx = rstd (n - mean_c n - xh mean_c(n xh))
+ *     d_weight = sum_tokens d_y xh      d_bias = sum_tokens d_y
+ *   x, weight, mean, rstd: as in the forward    d_y: [ntok,D] dy_dtype
+ *   dx: [ntok,D] dx_dtype, written in full (may not alias x or d_y)
+ *   d_weight, d_bias: [D] float32, both or neither NULL (not emitted); zeros
+ *          for ntok = 0
+ *   workspace: at least retention_layer_norm_bwd_workspace_size(...) bytes,
+ *          256-byte aligned, when d_weight is given (partial sums over tokens,
+ *          added in a fixed order: results are the same from run to run)
+ * Supported: as retention_layer_norm_fwd.
+ */
+RET_API size_t retention_layer_norm_bwd_workspace_size(int ntok, int D);
+RET_API ret_status retention_layer_norm_bwd(const void* x, ret_dtype x_dtype, const void* d_y,
+                                            ret_dtype dy_dtype, const float* mean,
+                                            const float* rstd, const float* weight, void* dx,
+                                            ret_dtype dx_dtype, float* d_weight, float* d_bias,
+                                            void* workspace, size_t workspace_bytes, int ntok,
+                                            int D, ret_stream_t stream);
+
+/*
+ * Gradients of msr_norm_gate (and of the epilogue that retention_chunkwise_fwd
+ * fuses, from its un-normalised output o).  With xh the normalised o, t = xh
+ * weight + bias, swish(g) = g sigmoid(g), and per (token, head) over dv channels:
+ *     d_g = d_y t sigmoid(g) (1 + g (1 - sigmoid(g)))
+ *     dt  = d_y swish(g),   n = dt weight
+ *     d_o = rstd (n - mean_c n - xh mean_c(n xh))
+ *     d_weight = sum_tokens dt xh       d_bias = sum_tokens dt
+ * The statistics of o are taken again; nothing of the forward but its inputs
+ * is read.
+ *   o: [ntok,H,dv] o_dtype    ng: as given to the forward; g_dtype is also the
+ *   dtype of d_y [ntok,H,dv]
+ *   d_o, d_g: [ntok,H,dv] grad_dtype, written in full (no aliasing with inputs)
+ *   d_weight, d_bias: [H*dv] float32, both or neither NULL; zeros for ntok = 0
+ *   workspace: at least msr_norm_gate_bwd_workspace_size(...) bytes, 256-byte
+ *          aligned, when d_weight is given (as retention_layer_norm_bwd)
+ * Supported: ntok >= 0, H >= 1, dv in 1..1024, H*dv <= 2^20; element offsets
+ * are 64-bit.
+ */
+RET_API size_t msr_norm_gate_bwd_workspace_size(int ntok, int H, int dv);
+RET_API ret_status msr_norm_gate_bwd(const void* o, ret_dtype o_dtype, const ret_norm_gate* ng,
+                                     const void* d_y, void* d_o, void* d_g, ret_dtype grad_dtype,
+                                     float* d_weight, float* d_bias, void* workspace,
+                                     size_t workspace_bytes, int ntok, int H, int dv,
+                                     ret_stream_t stream);
 
 /*
  * Synchronises `stream`, then reads and clears this device's error word, which

@@ -731,6 +731,201 @@ ret_status retention_check_device_error(ret_stream_t stream) {
 }  // extern "C"
 
 // ---------------------------------------------------------------------------
+// Gated linear recurrence, layer norm and the gradients of the norms
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int kMaxGlrChannels = 1 << 20;
+constexpr int kMaxNormRow = 16384;
+
+bool workspace_ok(const void* ws, size_t bytes, size_t need) {
+  return need == 0 ||
+         (ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 && bytes >= need);
+}
+
+// Sizes and packing of one gated-recurrence call.
+ret_status glr_layout(int B, int T, int D, const int32_t* cu, int nseq, ret::SeqLayout* L) {
+  if (nseq < 0 || D < 1) return RET_ERR_INVALID_ARG;
+  if (nseq > 0 ? (B != 1 || T < 0) : (B < 1 || T < 1)) return RET_ERR_INVALID_ARG;
+  const long long Ttot = nseq > 0 ? T : static_cast<long long>(B) * T;
+  if (!fits_int(Ttot + ret::kGlrChunk)) return RET_ERR_INVALID_ARG;
+  if (D > kMaxGlrChannels) return RET_ERR_UNSUPPORTED;
+  L->cu = cu;
+  L->nseq = nseq > 0 ? nseq : B;
+  L->T = nseq > 0 ? 0 : T;
+  L->Ttot = static_cast<int>(Ttot);
+  L->chunk = ret::kGlrChunk;
+  L->nslots = Ttot / ret::kGlrChunk + L->nseq;
+  return RET_OK;
+}
+
+bool gate_scale_ok(double c) { return std::isfinite(static_cast<float>(c)) && c > 0.0; }
+
+}  // namespace
+
+extern "C" {
+
+size_t retention_glr_chunk_slots(int B, int T, int nseq) {
+  ret::SeqLayout L;
+  if (glr_layout(B, T, 1, nullptr, nseq, &L) != RET_OK) return 0;
+  return static_cast<size_t>(L.nslots);
+}
+
+ret_status retention_glr_fwd(const void* x, const void* r, const void* i, ret_dtype in_dtype,
+                             const float* lam, double c, const int32_t* cu_seqlens, int nseq,
+                             const float* state_in, float* state_out, void* h, ret_dtype h_dtype,
+                             float* chunk_states, int B, int T, int D, ret_stream_t stream) {
+  if (!dtype_ok(in_dtype) || !dtype_ok(h_dtype) || !lam || !gate_scale_ok(c))
+    return RET_ERR_INVALID_ARG;
+  if ((cu_seqlens != nullptr) != (nseq > 0)) return RET_ERR_INVALID_ARG;
+  ret::SeqLayout L;
+  const ret_status st = glr_layout(B, T, D, cu_seqlens, nseq, &L);
+  if (st != RET_OK) return st;
+  if (L.Ttot > 0 && (!x || !r || !i || !h)) return RET_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, r, i, lam, cu_seqlens, state_in, state_out, h, chunk_states};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return RET_ERR_INVALID_ARG;
+  unsigned* err = error_word();
+  if (!err) return RET_ERR_CUDA;
+  return cuda_status(ret::launch_glr_fwd(x, r, i, dt(in_dtype), lam, static_cast<float>(c), L,
+                                         state_in, state_out, h, dt(h_dtype), chunk_states, D, err,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t retention_glr_bwd_workspace_size(int B, int T, int D, int nseq) {
+  ret::SeqLayout L;
+  if (glr_layout(B, T, D, nullptr, nseq, &L) != RET_OK) return 0;
+  return round256(static_cast<size_t>(ret::glr_bwd_partial_rows(L.nseq, L.Ttot, D)) * D *
+                  sizeof(float));
+}
+
+ret_status retention_glr_bwd(const void* x, const void* r, const void* i, ret_dtype in_dtype,
+                             const float* lam, double c, const int32_t* cu_seqlens, int nseq,
+                             const float* chunk_states, const void* d_h, ret_dtype dh_dtype,
+                             const float* d_state_out, void* dx, void* dr, void* di,
+                             ret_dtype grad_dtype, float* d_lam, float* d_state_in,
+                             void* workspace, size_t workspace_bytes, int B, int T, int D,
+                             ret_stream_t stream) {
+  if (!dtype_ok(in_dtype) || !dtype_ok(dh_dtype) || !dtype_ok(grad_dtype) || !lam || !d_lam ||
+      !gate_scale_ok(c))
+    return RET_ERR_INVALID_ARG;
+  if ((cu_seqlens != nullptr) != (nseq > 0)) return RET_ERR_INVALID_ARG;
+  ret::SeqLayout L;
+  const ret_status st = glr_layout(B, T, D, cu_seqlens, nseq, &L);
+  if (st != RET_OK) return st;
+  if (L.Ttot > 0 && (!x || !r || !i || !chunk_states || !d_h || !dx || !dr || !di))
+    return RET_ERR_INVALID_ARG;
+  const void* ptrs[] = {x,  r,  i,  lam, cu_seqlens, chunk_states, d_h,
+                        dx, dr, di, d_lam, d_state_out, d_state_in};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return RET_ERR_INVALID_ARG;
+  if (!workspace_ok(workspace, workspace_bytes,
+                    retention_glr_bwd_workspace_size(B, T, D, nseq)))
+    return RET_ERR_WORKSPACE;
+  unsigned* err = error_word();
+  if (!err) return RET_ERR_CUDA;
+  return cuda_status(ret::launch_glr_bwd(
+      x, r, i, dt(in_dtype), lam, static_cast<float>(c), L, chunk_states, d_h, dt(dh_dtype),
+      d_state_out, dx, dr, di, dt(grad_dtype), d_lam, d_state_in, static_cast<float*>(workspace),
+      D, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ret_status retention_glr_step(const void* x, const void* r, const void* i, ret_dtype in_dtype,
+                              const float* lam, double c, const float* state, float* state_out,
+                              void* h, ret_dtype h_dtype, int N, int D, ret_stream_t stream) {
+  if (!x || !r || !i || !lam || !state || !state_out || !dtype_ok(in_dtype) ||
+      !dtype_ok(h_dtype) || !gate_scale_ok(c) || N < 1 || D < 1)
+    return RET_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, r, i, lam, state, state_out, h};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return RET_ERR_INVALID_ARG;
+  if (D > kMaxGlrChannels) return RET_ERR_UNSUPPORTED;
+  return cuda_status(ret::launch_glr_step(x, r, i, dt(in_dtype), lam, static_cast<float>(c), state,
+                                          state_out, h, dt(h_dtype), N, D,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ret_status retention_layer_norm_fwd(const void* x, ret_dtype x_dtype, const float* weight,
+                                    const float* bias, double eps, void* y, ret_dtype y_dtype,
+                                    float* mean, float* rstd, int ntok, int D,
+                                    ret_stream_t stream) {
+  if (!dtype_ok(x_dtype) || !dtype_ok(y_dtype) || ntok < 0 || D < 1 ||
+      !std::isfinite(static_cast<float>(eps)) || eps < 0.0)
+    return RET_ERR_INVALID_ARG;
+  if (ntok > 0 && (!x || !y)) return RET_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, weight, bias, y, mean, rstd};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return RET_ERR_INVALID_ARG;
+  if (D > kMaxNormRow) return RET_ERR_UNSUPPORTED;
+  if (ntok == 0) return RET_OK;
+  return cuda_status(ret::launch_layer_norm_fwd(x, dt(x_dtype), weight, bias,
+                                                static_cast<float>(eps), y, dt(y_dtype), mean,
+                                                rstd, ntok, D,
+                                                reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t retention_layer_norm_bwd_workspace_size(int ntok, int D) {
+  if (ntok < 0 || D < 1 || D > kMaxNormRow) return 0;
+  return round256(2 * static_cast<size_t>(ret::layer_norm_bwd_partial_rows(ntok, D)) * D *
+                  sizeof(float));
+}
+
+ret_status retention_layer_norm_bwd(const void* x, ret_dtype x_dtype, const void* d_y,
+                                    ret_dtype dy_dtype, const float* mean, const float* rstd,
+                                    const float* weight, void* dx, ret_dtype dx_dtype,
+                                    float* d_weight, float* d_bias, void* workspace,
+                                    size_t workspace_bytes, int ntok, int D,
+                                    ret_stream_t stream) {
+  if (!dtype_ok(x_dtype) || !dtype_ok(dy_dtype) || !dtype_ok(dx_dtype) || ntok < 0 || D < 1 ||
+      (d_weight == nullptr) != (d_bias == nullptr))
+    return RET_ERR_INVALID_ARG;
+  if (ntok > 0 && (!x || !d_y || !mean || !rstd || !dx)) return RET_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, d_y, mean, rstd, weight, dx, d_weight, d_bias};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return RET_ERR_INVALID_ARG;
+  if (D > kMaxNormRow) return RET_ERR_UNSUPPORTED;
+  if (d_weight && !workspace_ok(workspace, workspace_bytes,
+                                retention_layer_norm_bwd_workspace_size(ntok, D)))
+    return RET_ERR_WORKSPACE;
+  return cuda_status(ret::launch_layer_norm_bwd(
+      x, dt(x_dtype), d_y, dt(dy_dtype), mean, rstd, weight, dx, dt(dx_dtype), d_weight, d_bias,
+      static_cast<float*>(workspace), ntok, D, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t msr_norm_gate_bwd_workspace_size(int ntok, int H, int dv) {
+  if (ntok < 0 || H < 1 || dv < 1 || dv > 1024 ||
+      static_cast<long long>(H) * dv > kMaxGlrChannels)
+    return 0;
+  return round256(2 * static_cast<size_t>(ret::norm_gate_bwd_partial_rows(ntok, H, dv)) * H * dv *
+                  sizeof(float));
+}
+
+ret_status msr_norm_gate_bwd(const void* o, ret_dtype o_dtype, const ret_norm_gate* ng,
+                             const void* d_y, void* d_o, void* d_g, ret_dtype grad_dtype,
+                             float* d_weight, float* d_bias, void* workspace,
+                             size_t workspace_bytes, int ntok, int H, int dv,
+                             ret_stream_t stream) {
+  if (!ng || !dtype_ok(o_dtype) || !dtype_ok(ng->g_dtype) || !dtype_ok(grad_dtype) || ntok < 0 ||
+      H < 1 || dv < 1 || (d_weight == nullptr) != (d_bias == nullptr))
+    return RET_ERR_INVALID_ARG;
+  if (ntok > 0 && (!o || !ng->g || !d_y || !d_o || !d_g)) return RET_ERR_INVALID_ARG;
+  if (!std::isfinite(ng->eps) || ng->eps < 0.f) return RET_ERR_INVALID_ARG;
+  const void* ptrs[] = {o, ng->g, ng->weight, ng->bias, d_y, d_o, d_g, d_weight, d_bias};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return RET_ERR_INVALID_ARG;
+  if (dv > 1024 || static_cast<long long>(H) * dv > kMaxGlrChannels) return RET_ERR_UNSUPPORTED;
+  if (d_weight && !workspace_ok(workspace, workspace_bytes,
+                                msr_norm_gate_bwd_workspace_size(ntok, H, dv)))
+    return RET_ERR_WORKSPACE;
+  return cuda_status(ret::launch_norm_gate_bwd(
+      o, dt(o_dtype), ng->g, d_y, dt(ng->g_dtype), ng->weight, ng->bias, ng->eps, d_o, d_g,
+      dt(grad_dtype), d_weight, d_bias, static_cast<float*>(workspace), ntok, H, dv,
+      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
 // Chunkwise forward that allocates nothing: its scratch is a file-scope
 // device array of RETENTION_STATIC_WORKSPACE_BYTES, present on every device
 // that loads this library for as long as the library stays loaded.

@@ -113,6 +113,41 @@ cudaError_t launch_norm_gate(const void* o, DType o_t, const void* g, DType g_t,
 // Tensor-core (tcgen05) chunkwise forward for bf16 inputs.
 bool chunkwise_tc_supported(int dk, int dv, int chunk);
 
+// Gated linear recurrence: forward, gradients (partial: float32 scratch of
+// glr_bwd_partial_rows(L, D) rows of D) and the one-token step.
+constexpr int kGlrChunk = 64;      // tokens between two stored states
+cudaError_t launch_glr_fwd(const void* x, const void* r, const void* i, DType in_t,
+                           const float* lam, float c, const SeqLayout& L, const float* state_in,
+                           float* state_out, void* h, DType h_t, float* chunk_states, int D,
+                           unsigned* err, cudaStream_t s);
+long long glr_bwd_partial_rows(int nseq, long long Ttot, int D);
+cudaError_t launch_glr_bwd(const void* x, const void* r, const void* i, DType in_t,
+                           const float* lam, float c, const SeqLayout& L,
+                           const float* chunk_states, const void* d_h, DType dh_t,
+                           const float* d_state_out, void* dx, void* dr, void* di, DType g_t,
+                           float* d_lam, float* d_state_in, float* partial, int D, unsigned* err,
+                           cudaStream_t s);
+cudaError_t launch_glr_step(const void* x, const void* r, const void* i, DType in_t,
+                            const float* lam, float c, const float* state, float* state_out,
+                            void* h, DType h_t, int N, int D, cudaStream_t s);
+
+// Layer norm and its gradients; the gradients of the GroupNorm + gate.
+// `partial` holds *_bwd_partial_rows(...) rows of d_weight, then as many of
+// d_bias (float32, as wide as the weights).
+cudaError_t launch_layer_norm_fwd(const void* x, DType x_t, const float* w, const float* b,
+                                  float eps, void* y, DType y_t, float* mean, float* rstd,
+                                  int ntok, int D, cudaStream_t s);
+int layer_norm_bwd_partial_rows(int ntok, int D);
+cudaError_t launch_layer_norm_bwd(const void* x, DType x_t, const void* dy, DType dy_t,
+                                  const float* mean, const float* rstd, const float* w, void* dx,
+                                  DType dx_t, float* dw, float* db, float* partial, int ntok,
+                                  int D, cudaStream_t s);
+int norm_gate_bwd_partial_rows(int ntok, int H, int dv);
+cudaError_t launch_norm_gate_bwd(const void* o, DType o_t, const void* g, const void* dy,
+                                 DType g_t, const float* w, const float* b, float eps, void* d_o,
+                                 void* d_g, DType grad_t, float* dw, float* db, float* partial,
+                                 int ntok, int H, int dv, cudaStream_t s);
+
 // One bounded wait that is never satisfied (failure-detection self-test).
 cudaError_t launch_wait_timeout_selftest(unsigned* err, cudaStream_t s);
 int chunkwise_tc_chunk(int chunk, int dv);  // chunk length the kernels evaluate

@@ -8,6 +8,7 @@ is no CPU or PyTorch fallback, and calling any function without the built
 library raises immediately.
 """
 
+import contextlib
 import ctypes
 import os
 
@@ -32,6 +33,9 @@ RET_BF16 = 1
 # Capacity of the library's built-in scratch (RETENTION_STATIC_WORKSPACE_BYTES).
 STATIC_WORKSPACE_BYTES = 32 << 20
 
+# Tokens between two stored states of the gated linear recurrence (RETENTION_GLR_CHUNK).
+GLR_CHUNK = 64
+
 EXPORTED = (
     "retention_abi_version",
     "retention_source_sha",
@@ -54,6 +58,16 @@ EXPORTED = (
     "retention_recurrent_step",
     "retention_recurrent_steps",
     "msr_norm_gate",
+    "retention_glr_chunk_slots",
+    "retention_glr_fwd",
+    "retention_glr_bwd_workspace_size",
+    "retention_glr_bwd",
+    "retention_glr_step",
+    "retention_layer_norm_fwd",
+    "retention_layer_norm_bwd_workspace_size",
+    "retention_layer_norm_bwd",
+    "msr_norm_gate_bwd_workspace_size",
+    "msr_norm_gate_bwd",
     "retention_check_device_error",
     "retention_selftest_wait_timeout",
 )
@@ -154,6 +168,31 @@ def lib():
     L.retention_recurrent_steps.argtypes = [vp, vp, vp, ci, cd, vp, vp, ci, ci, ci, ci, ci, ci, vp]
     L.msr_norm_gate.restype = ci
     L.msr_norm_gate.argtypes = [vp, ci, ctypes.POINTER(NormGate), vp, ci, ci, ci, ci, vp]
+    cf, cs = ctypes.c_double, ctypes.c_size_t
+    L.retention_glr_chunk_slots.restype = cs
+    L.retention_glr_chunk_slots.argtypes = [ci, ci, ci]
+    L.retention_glr_fwd.restype = ci
+    L.retention_glr_fwd.argtypes = [vp, vp, vp, ci, vp, cf, vp, ci, vp, vp, vp, ci, vp,
+                                    ci, ci, ci, vp]
+    L.retention_glr_bwd_workspace_size.restype = cs
+    L.retention_glr_bwd_workspace_size.argtypes = [ci, ci, ci, ci]
+    L.retention_glr_bwd.restype = ci
+    L.retention_glr_bwd.argtypes = [vp, vp, vp, ci, vp, cf, vp, ci, vp, vp, ci, vp, vp, vp, vp, ci,
+                                    vp, vp, vp, cs, ci, ci, ci, vp]
+    L.retention_glr_step.restype = ci
+    L.retention_glr_step.argtypes = [vp, vp, vp, ci, vp, cf, vp, vp, vp, ci, ci, ci, vp]
+    L.retention_layer_norm_fwd.restype = ci
+    L.retention_layer_norm_fwd.argtypes = [vp, ci, vp, vp, cf, vp, ci, vp, vp, ci, ci, vp]
+    L.retention_layer_norm_bwd_workspace_size.restype = cs
+    L.retention_layer_norm_bwd_workspace_size.argtypes = [ci, ci]
+    L.retention_layer_norm_bwd.restype = ci
+    L.retention_layer_norm_bwd.argtypes = [vp, ci, vp, ci, vp, vp, vp, vp, ci, vp, vp, vp, cs,
+                                           ci, ci, vp]
+    L.msr_norm_gate_bwd_workspace_size.restype = cs
+    L.msr_norm_gate_bwd_workspace_size.argtypes = [ci, ci, ci]
+    L.msr_norm_gate_bwd.restype = ci
+    L.msr_norm_gate_bwd.argtypes = [vp, ci, ctypes.POINTER(NormGate), vp, vp, vp, ci, vp, vp, vp,
+                                    cs, ci, ci, ci, vp]
     L.retention_check_device_error.restype = ci
     L.retention_check_device_error.argtypes = [vp]
     L.retention_selftest_wait_timeout.restype = ci
@@ -604,6 +643,256 @@ def norm_gate(o, g, weight=None, bias=None, eps=1e-5, out_dtype=None, out=None, 
                              _stream(stream))
     _check(st, "msr_norm_gate")
     return y
+
+
+def _ready(stream, **tensors):
+    """Checks the tensors of one call (None allowed): contiguous CUDA tensors, all on the
+    current device, as is ``stream``."""
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for name, t in tensors.items():
+        if t is not None:
+            _dev(t, name)
+            if t.device.index != cur:
+                raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+    if stream is not None and stream.device.index != cur:
+        raise ValueError(f"stream is on {stream.device}, the current device is cuda:{cur}")
+
+
+def _alloc_on(stream):
+    """Context in which new tensors belong to the stream the kernels will run on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _shaped(t, name, shape, dtype=None):
+    if t is not None and (tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype)):
+        kind = "" if dtype is None else f"{str(dtype)[6:]} "
+        raise ValueError(f"{name} must be {kind}{list(shape)}")
+
+
+def _offsets(cu_seqlens):
+    if cu_seqlens is None:
+        return 0
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be a 1-D int32 tensor with at least two entries")
+    return cu_seqlens.numel() - 1
+
+
+def glr_chunk_slots(B, T, nseq=0):
+    """Rows of ``chunk_states`` for these sizes (0 if they are invalid)."""
+    return int(lib().retention_glr_chunk_slots(B, T, nseq))
+
+
+def _glr_inputs(x, r, i, lam, cu_seqlens):
+    if x.dim() != 3 or r.shape != x.shape or i.shape != x.shape or not x.dtype == r.dtype == i.dtype:
+        raise ValueError("x, r, i must have one [B,T,D] shape and one dtype")
+    B, T, D = x.shape
+    _shaped(lam, "lam", (D,), torch.float32)
+    nseq = _offsets(cu_seqlens)
+    if nseq and B != 1:
+        raise ValueError("packed sequences need B = 1")
+    return B, T, D, nseq
+
+
+def glr_fwd(x, r, i, lam, c=8.0, cu_seqlens=None, state_in=None, return_state=False,
+            return_chunks=False, out_dtype=None, out=None, state_out=None, chunk_states=None,
+            stream=None):
+    """Gated linear recurrence h_t = a_t h_(t-1) + sqrt(1 - a_t^2) sigmoid(i_t) x_t with
+    a_t = exp(-c softplus(lam) sigmoid(r_t)) (retention_glr_fwd).
+
+    x, r, i: [B,T,D], one dtype; lam: float32 [D]; packed sequences: B = 1 and ``cu_seqlens``
+    as in :func:`chunkwise_fwd`.  ``state_in`` / ``state_out``: float32 [nseq|B,D].  Returns
+    ``h`` [B,T,D], then the final states with ``return_state``, then with ``return_chunks``
+    the states entering every 64 tokens (float32 [slots,D]), which :func:`glr_bwd` takes.
+    """
+    _ready(stream, x=x, r=r, i=i, lam=lam, cu_seqlens=cu_seqlens, state_in=state_in, out=out,
+           state_out=state_out, chunk_states=chunk_states)
+    B, T, D, nseq = _glr_inputs(x, r, i, lam, cu_seqlens)
+    states = (nseq or B, D)
+    slots = (glr_chunk_slots(B, T, nseq), D) if return_chunks or chunk_states is not None else None
+    _shaped(state_in, "state_in", states, torch.float32)
+    _shaped(state_out, "state_out", states, torch.float32)
+    _shaped(out, "out", x.shape, out_dtype)
+    _shaped(chunk_states, "chunk_states", slots, torch.float32)
+    with _alloc_on(stream):
+        if out is None:
+            out = torch.empty(x.shape, device=x.device, dtype=out_dtype or x.dtype)
+        if return_state and state_out is None:
+            state_out = torch.empty(states, device=x.device, dtype=torch.float32)
+        if return_chunks and chunk_states is None:
+            chunk_states = torch.empty(slots, device=x.device, dtype=torch.float32)
+    st = lib().retention_glr_fwd(_ptr(x), _ptr(r), _ptr(i), _dt(x), _ptr(lam), float(c),
+                                 _ptr(cu_seqlens), nseq, _ptr(state_in), _ptr(state_out),
+                                 _ptr(out), _dt(out), _ptr(chunk_states), B, T, D,
+                                 _stream(stream))
+    _check(st, "retention_glr_fwd")
+    if not (return_state or return_chunks):
+        return out
+    return (out,) + ((state_out,) if return_state else ()) + (
+        (chunk_states,) if return_chunks else ())
+
+
+def glr_bwd_workspace_size(B, T, D, nseq=0):
+    return int(lib().retention_glr_bwd_workspace_size(B, T, D, nseq))
+
+
+def glr_bwd(x, r, i, lam, chunk_states, d_h, c=8.0, cu_seqlens=None, d_state_out=None,
+            return_d_state=False, grad_dtype=None, workspace=None, stream=None):
+    """Gradients of :func:`glr_fwd` (retention_glr_bwd).
+
+    ``chunk_states`` are the forward's (``return_chunks``), ``d_h`` [B,T,D] the gradient of h
+    and ``d_state_out`` (float32 [nseq|B,D], optional) that of the final states.  Returns
+    ``(dx, dr, di, d_lam)``, the first three in ``grad_dtype`` (default: x's dtype), and with
+    ``return_d_state`` the gradient of the initial states.
+    """
+    _ready(stream, x=x, r=r, i=i, lam=lam, chunk_states=chunk_states, d_h=d_h,
+           cu_seqlens=cu_seqlens, d_state_out=d_state_out, workspace=workspace)
+    B, T, D, nseq = _glr_inputs(x, r, i, lam, cu_seqlens)
+    states = (nseq or B, D)
+    _shaped(d_h, "d_h", x.shape)
+    _shaped(chunk_states, "chunk_states", (glr_chunk_slots(B, T, nseq), D), torch.float32)
+    _shaped(d_state_out, "d_state_out", states, torch.float32)
+    need = glr_bwd_workspace_size(B, T, D, nseq)
+    with _alloc_on(stream):
+        dx, dr, di = (torch.empty(x.shape, device=x.device, dtype=grad_dtype or x.dtype)
+                      for _ in range(3))
+        d_lam = torch.empty(D, device=x.device, dtype=torch.float32)
+        dS = torch.empty(states, device=x.device, dtype=torch.float32) if return_d_state else None
+        if workspace is None:
+            workspace = alloc_workspace(need, x.device)
+    st = lib().retention_glr_bwd(_ptr(x), _ptr(r), _ptr(i), _dt(x), _ptr(lam), float(c),
+                                 _ptr(cu_seqlens), nseq, _ptr(chunk_states), _ptr(d_h), _dt(d_h),
+                                 _ptr(d_state_out), _ptr(dx), _ptr(dr), _ptr(di), _dt(dx),
+                                 _ptr(d_lam), _ptr(dS), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), B, T, D,
+                                 _stream(stream))
+    _check(st, "retention_glr_bwd")
+    return (dx, dr, di, d_lam, dS) if return_d_state else (dx, dr, di, d_lam)
+
+
+def glr_step(x, r, i, lam, state, c=8.0, out_dtype=torch.float32, out=None, state_out=None,
+             stream=None):
+    """One token of the gated linear recurrence for N sequences: x, r, i [N,D], ``state``
+    float32 [N,D], updated in place unless ``state_out`` is given.  Returns h [N,D]."""
+    _ready(stream, x=x, r=r, i=i, lam=lam, state=state, out=out, state_out=state_out)
+    if x.dim() != 2 or r.shape != x.shape or i.shape != x.shape or not x.dtype == r.dtype == i.dtype:
+        raise ValueError("x, r, i must have one [N,D] shape and one dtype")
+    N, D = x.shape
+    _shaped(lam, "lam", (D,), torch.float32)
+    _shaped(state, "state", (N, D), torch.float32)
+    _shaped(state_out, "state_out", (N, D), torch.float32)
+    _shaped(out, "out", (N, D))
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty(N, D, device=x.device, dtype=out_dtype)
+    if state_out is None:
+        state_out = state
+    st = lib().retention_glr_step(_ptr(x), _ptr(r), _ptr(i), _dt(x), _ptr(lam), float(c),
+                                  _ptr(state), _ptr(state_out), _ptr(out), _dt(out), N, D,
+                                  _stream(stream))
+    _check(st, "retention_glr_step")
+    return out
+
+
+def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out_dtype=None, out=None,
+                   return_stats=False, stream=None):
+    """Layer norm over the last dimension (retention_layer_norm_fwd); x: [...,D], weight and
+    bias: float32 [D] or None.  Returns y and, with ``return_stats``, the float32 mean and
+    1/sqrt(var + eps) of every row, which :func:`layer_norm_bwd` takes."""
+    _ready(stream, x=x, weight=weight, bias=bias, out=out)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must have a last dimension to normalise")
+    D = x.shape[-1]
+    ntok = x.numel() // D
+    _shaped(weight, "weight", (D,), torch.float32)
+    _shaped(bias, "bias", (D,), torch.float32)
+    _shaped(out, "out", x.shape, out_dtype)
+    mean = rstd = None
+    with _alloc_on(stream):
+        if out is None:
+            out = torch.empty(x.shape, device=x.device, dtype=out_dtype or x.dtype)
+        if return_stats:
+            mean = torch.empty(x.shape[:-1], device=x.device, dtype=torch.float32)
+            rstd = torch.empty(x.shape[:-1], device=x.device, dtype=torch.float32)
+    st = lib().retention_layer_norm_fwd(_ptr(x), _dt(x), _ptr(weight), _ptr(bias), float(eps),
+                                        _ptr(out), _dt(out), _ptr(mean), _ptr(rstd), ntok, D,
+                                        _stream(stream))
+    _check(st, "retention_layer_norm_fwd")
+    return (out, mean, rstd) if return_stats else out
+
+
+def layer_norm_bwd_workspace_size(ntok, D):
+    return int(lib().retention_layer_norm_bwd_workspace_size(ntok, D))
+
+
+def layer_norm_bwd(x, d_y, mean, rstd, weight=None, return_d_affine=True, grad_dtype=None,
+                   workspace=None, stream=None):
+    """Gradients of :func:`layer_norm_fwd` (retention_layer_norm_bwd); ``mean`` and ``rstd`` as
+    the forward returned them.  Returns ``(dx, d_weight, d_bias)`` (dx in ``grad_dtype``,
+    default x's; the others float32 [D]), or dx alone without ``return_d_affine``."""
+    _ready(stream, x=x, d_y=d_y, mean=mean, rstd=rstd, weight=weight, workspace=workspace)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must have a last dimension to normalise")
+    D = x.shape[-1]
+    ntok = x.numel() // D
+    _shaped(d_y, "d_y", x.shape)
+    _shaped(mean, "mean", x.shape[:-1], torch.float32)
+    _shaped(rstd, "rstd", x.shape[:-1], torch.float32)
+    _shaped(weight, "weight", (D,), torch.float32)
+    dw = db = None
+    with _alloc_on(stream):
+        dx = torch.empty(x.shape, device=x.device, dtype=grad_dtype or x.dtype)
+        if return_d_affine:
+            dw = torch.empty(D, device=x.device, dtype=torch.float32)
+            db = torch.empty(D, device=x.device, dtype=torch.float32)
+            if workspace is None:
+                workspace = alloc_workspace(layer_norm_bwd_workspace_size(ntok, D), x.device)
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = lib().retention_layer_norm_bwd(_ptr(x), _dt(x), _ptr(d_y), _dt(d_y), _ptr(mean),
+                                        _ptr(rstd), _ptr(weight), _ptr(dx), _dt(dx), _ptr(dw),
+                                        _ptr(db), _ptr(workspace), nbytes, ntok, D,
+                                        _stream(stream))
+    _check(st, "retention_layer_norm_bwd")
+    return (dx, dw, db) if return_d_affine else dx
+
+
+def norm_gate_bwd_workspace_size(ntok, H, dv):
+    return int(lib().msr_norm_gate_bwd_workspace_size(ntok, H, dv))
+
+
+def norm_gate_bwd(o, g, d_y, weight=None, bias=None, eps=1e-5, return_d_affine=True,
+                  grad_dtype=None, workspace=None, stream=None):
+    """Gradients of :func:`norm_gate` (msr_norm_gate_bwd); o and d_y: [...,H,dv], g the same
+    size and d_y's dtype.  Returns ``(d_o, d_g, d_weight, d_bias)``: the first two in
+    ``grad_dtype`` (default d_y's) and shaped as o and g, the others float32 [H*dv] and left
+    out without ``return_d_affine``.  d_o is the ``d_out`` of :func:`chunkwise_bwd`."""
+    _ready(stream, o=o, g=g, d_y=d_y, weight=weight, bias=bias, workspace=workspace)
+    if o.dim() < 2 or min(o.shape[-2:]) < 1:
+        raise ValueError("o must be [...,H,dv]")
+    H, dv = o.shape[-2], o.shape[-1]
+    ntok = o.numel() // (H * dv)
+    _shaped(d_y, "d_y", o.shape)
+    if g.numel() != o.numel() or g.dtype != d_y.dtype:
+        raise ValueError("g must have as many elements as o and d_y's dtype")
+    for t, n in ((weight, "weight"), (bias, "bias")):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != H * dv):
+            raise ValueError(f"{n} must be float32 with H*dv elements")
+    dw = db = None
+    with _alloc_on(stream):
+        d_o = torch.empty(o.shape, device=o.device, dtype=grad_dtype or d_y.dtype)
+        d_g = torch.empty(g.shape, device=o.device, dtype=grad_dtype or d_y.dtype)
+        if return_d_affine:
+            dw = torch.empty(H * dv, device=o.device, dtype=torch.float32)
+            db = torch.empty(H * dv, device=o.device, dtype=torch.float32)
+            if workspace is None:
+                workspace = alloc_workspace(norm_gate_bwd_workspace_size(ntok, H, dv), o.device)
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ng = NormGate(g.data_ptr(), _dt(g), weight.data_ptr() if weight is not None else None,
+                  bias.data_ptr() if bias is not None else None, float(eps))
+    st = lib().msr_norm_gate_bwd(_ptr(o), _dt(o), ctypes.byref(ng), _ptr(d_y), _ptr(d_o),
+                                 _ptr(d_g), _dt(d_o), _ptr(dw), _ptr(db), _ptr(workspace), nbytes,
+                                 ntok, H, dv, _stream(stream))
+    _check(st, "msr_norm_gate_bwd")
+    return (d_o, d_g, dw, db) if return_d_affine else (d_o, d_g)
 
 
 def check_device_error(stream=None):

@@ -84,6 +84,12 @@ __all__ = [
     "rope",
     "softmax_features",
     "rla",
+    "glr",
+    "glr_backward",
+    "glr_chunk_states",
+    "layer_norm",
+    "layer_norm_backward",
+    "norm_gate_backward",
 ]
 
 
@@ -499,3 +505,126 @@ def rla(q, k, v, window, cu_seqlens=None):
                     S = S + np.outer(fk[b, m, h], v[b, m, h])
                     o[b, t, h] = fq[b, t, h] @ S
     return o
+
+
+# ---------------------------------------------------------------------------
+# Gated linear recurrence: a vector state whose decay depends on the token
+# ---------------------------------------------------------------------------
+
+def _sigmoid(x):
+    return np.exp(-np.logaddexp(0.0, -_f64(x)))
+
+
+def _segments(B, T, cu_seqlens):
+    return ([(b, b, 0, T) for b in range(B)] if cu_seqlens is None else
+            [(s, 0, int(a), int(e)) for s, (a, e) in enumerate(zip(cu_seqlens[:-1], cu_seqlens[1:]))])
+
+
+def _glr_gates(r, i, lam, c):
+    """y = c softplus(lam) sigmoid(r), a = exp(-y), root = sqrt(1 - a^2), sigmoid(i)."""
+    y = c * np.logaddexp(0.0, _f64(lam)) * _sigmoid(r)
+    return y, np.exp(-y), np.sqrt(-np.expm1(-2.0 * y)), _sigmoid(i)
+
+
+def glr(x, r, i, lam, c=8.0, state=None, cu_seqlens=None):
+    """Gated linear recurrence of ``x, r, i: [B,T,D]``, token by token.
+
+    The Griffin/Hawk page (section "Hawk") states h_t = a_t . h_(t-1) + b_t . x_t
+    with gates computed from the token; the gates read here are
+    a = exp(-c softplus(lam) sigmoid(r)), b = sqrt(1 - a^2) sigmoid(i).
+    ``state: [nseq|B, D]`` (None: zeros).  Returns ``h [B,T,D]`` and the final
+    states.
+    """
+    x = _f64(x)
+    _, a, root, si = _glr_gates(r, i, lam, c)
+    v = root * si * x
+    B, T, D = x.shape
+    segs = _segments(B, T, cu_seqlens)
+    S = np.zeros((len(segs), D)) if state is None else _f64(state).copy()
+    h = np.zeros_like(x)
+    for s, b, t0, t1 in segs:
+        for t in range(t0, t1):
+            S[s] = a[b, t] * S[s] + v[b, t]
+            h[b, t] = S[s]
+    return h, S
+
+
+def glr_chunk_states(h, state, chunk, cu_seqlens=None):
+    """The state entering every ``chunk`` tokens: {(sequence, chunk index): vector}."""
+    B, T, _ = h.shape
+    out = {}
+    for s, b, t0, t1 in _segments(B, T, cu_seqlens):
+        for j, t in enumerate(range(t0, t1, chunk)):
+            out[s, j] = state[s] if t == t0 else h[b, t - 1]
+    return out
+
+
+def glr_backward(x, r, i, lam, d_h, c=8.0, state=None, d_state=None, cu_seqlens=None):
+    """Gradients of :func:`glr`, token by token from the last.
+
+    With e_(T+1) = d_state: G_t = dh_t + e_(t+1), e_t = a_t G_t and
+        dx = G root si,   di = G root si' x,   dy = G (-a h_(t-1) + si x a^2 / root)
+        dr = dy y',       dlam = sum dy c sigmoid(lam) sigmoid(r)
+    (si' and y' the derivatives of the sigmoids; d root / dy = a^2 / root; where
+    root = 0 the product y / root is its limit 0).  Returns
+    ``(dx, dr, di, dlam [D], d_state_in)``.
+    """
+    x, dh = _f64(x), _f64(d_h)
+    y, a, root, si = _glr_gates(r, i, lam, c)
+    sr, sl = _sigmoid(r), _sigmoid(lam)
+    h, _ = glr(x, r, i, lam, c, state, cu_seqlens)
+    B, T, D = x.shape
+    segs = _segments(B, T, cu_seqlens)
+    S0 = np.zeros((len(segs), D)) if state is None else _f64(state)
+    e = np.zeros((len(segs), D)) if d_state is None else _f64(d_state).copy()
+    G, hp = np.zeros_like(x), np.zeros_like(x)
+    for s, b, t0, t1 in segs:
+        for t in range(t1 - 1, t0 - 1, -1):
+            G[b, t] = dh[b, t] + e[s]
+            e[s] = a[b, t] * G[b, t]
+            hp[b, t] = h[b, t - 1] if t > t0 else S0[s]
+    with np.errstate(divide="ignore", invalid="ignore"):
+        per_y = np.where(root > 0, y / root, 0.0)               # y d root / dy = per_y a^2
+    dyy = G * (per_y * a ** 2 * si * x - a * y * hp)             # y dL/dy
+    sp = np.logaddexp(0.0, _f64(lam))
+    dlam = dyy.sum(axis=(0, 1)) * np.where(sp > 0, sl / np.where(sp > 0, sp, 1.0), 1.0)
+    return G * root * si, dyy * (1.0 - sr), G * root * si * (1.0 - si) * x, dlam, e
+
+
+# ---------------------------------------------------------------------------
+# Layer norm, and the gradients of the norms
+# ---------------------------------------------------------------------------
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5):
+    """Layer norm over the last axis (biased variance): one group of all channels."""
+    x = _f64(x)
+    return group_norm_heads(x, eps, weight, bias)
+
+
+def layer_norm_backward(x, d_y, weight=None, eps=1e-5):
+    """Gradients of :func:`layer_norm`: ``(dx, d_weight, d_bias)``, the last two summed over
+    every leading axis.  dx = rstd (n - mean n - xh mean(n xh)) with n = d_y weight."""
+    x, dy = _f64(x), _f64(d_y)
+    xc = x - x.mean(axis=-1, keepdims=True)
+    rstd = 1.0 / np.sqrt((xc ** 2).mean(axis=-1, keepdims=True) + eps)
+    xh = xc * rstd
+    n = dy if weight is None else dy * _f64(weight)
+    dx = rstd * (n - n.mean(axis=-1, keepdims=True) - xh * (n * xh).mean(axis=-1, keepdims=True))
+    lead = tuple(range(x.ndim - 1))
+    return dx, (dy * xh).sum(axis=lead), dy.sum(axis=lead)
+
+
+def norm_gate_backward(o, g, d_y, eps=1e-5, weight=None, bias=None):
+    """Gradients of :func:`norm_gate` for ``o: [..., H, d_v]``:
+    ``(d_o, d_g, d_weight [H,d_v], d_bias [H,d_v])``."""
+    o, dy = _f64(o), _f64(d_y)
+    g = _f64(g).reshape(o.shape)
+    sg = _sigmoid(g)
+    t = group_norm_heads(o, eps, weight, bias)
+    d_g = dy * t * sg * (1.0 + g * (1.0 - sg))
+    H, dv = o.shape[-2:]
+    w = np.ones((H, dv)) if weight is None else _f64(weight).reshape(H, dv)
+    dt = dy * swish(g)
+    heads = [layer_norm_backward(o[..., h, :], dt[..., h, :], w[h], eps) for h in range(H)]
+    d_o = np.stack([x[0] for x in heads], axis=-2)
+    return d_o, d_g, np.stack([x[1] for x in heads]), np.stack([x[2] for x in heads])
