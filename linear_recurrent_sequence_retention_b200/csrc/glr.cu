@@ -35,9 +35,17 @@ constexpr int kMaxSplit = 16;       // CTAs of a cluster
 // How a lane's two channels lie and how rows reach shared memory.
 //   kWide: channels 2l, 2l+1; rows are copied in 16-byte pieces (D e bytes divide by 16)
 //   kEven: channels 2l, 2l+1; 4-byte pieces (D even)
-//   kOdd:  channels l, l+32; float32 in 4-byte pieces, bf16 read straight from global
-//          memory (its rows start at odd multiples of two bytes)
+//   kOdd:  channels l, l+32; 4-byte pieces; a bf16 row may start in the middle of one and
+//          then takes 33 of them
 enum { kWide = 0, kEven = 1, kOdd = 2 };
+
+// ---- pairs of floats (one instruction for both) ------------------------------
+
+using F2 = float2;
+__device__ __forceinline__ F2 f2(float x) { return make_float2(x, x); }
+__device__ __forceinline__ F2 mul(F2 a, F2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ F2 add(F2 a, F2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) { return __ffma2_rn(a, b, c); }
 
 // ---- gates -----------------------------------------------------------------
 
@@ -46,48 +54,56 @@ __device__ __forceinline__ float softplus(float x) {
 }
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float rsqrt_approx(float x) {
   float y;
-  asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float sigmoid(float x) {
-  return rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * x));
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ F2 sigmoid(F2 x) {
+  const F2 n = mul(x, f2(-1.4426950408889634f));
+  const F2 d = add(make_float2(ex2_approx(n.x), ex2_approx(n.y)), f2(1.f));
+  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
 
 // a = exp(-y) and root = sqrt(1 - a^2) for y >= 0, both to a few units of their
-// own last place: -y = n ln 2 + f, |f| <= ln 2 / 2, and with p = e^f - 1 (Taylor;
-// the eighth term is below 2^-25 of the first) a = 2^n p + 2^n and
-// 1 - a = 1 - 2^n - 2^n p, so 1 - a^2 = (1 - a)(1 + a) cancels nothing for decays
-// near one.  Above y = 87 a counts as zero (it is below 1.7e-38); below the
-// normal range of 1 - a^2 root is zero.
-__device__ __forceinline__ void decay(float y, float& a, float& root) {
+// own last place.  y = n ln 2 + g, |g| <= ln 2 / 2, and with w = 1 - e^-g (Taylor;
+// the eighth term is below 2^-25 of the first) a = 2^-n - 2^-n w and
+// 1 - a = 1 - 2^-n + 2^-n w, so 1 - a^2 = (1 - a)(1 + a) cancels nothing for decays
+// near one.  From n = 127 on (y above 87.7, a below 8e-39) 2^-n is taken as zero,
+// and root is zero where 1 - a^2 is below the normal range.
+__device__ __forceinline__ void decay(F2 y, F2& a, F2& root) {
   constexpr float kMagic = 12582912.f;           // 1.5 * 2^23: adding it rounds to an integer
-  const bool gone = y > 87.f;                    // NaN stays
-  y = gone ? 87.f : y;
-  const float m = fmaf(y, -1.4426950408889634f, kMagic);
-  const float n = m - kMagic;
-  float f = fmaf(n, -0.693147182464599609375f, -y);   // ln 2 in two parts
-  f = fmaf(n, 1.904654290582768e-9f, f);
-  float p = fmaf(f, 1.f / 5040.f, 1.f / 720.f);
-  p = fmaf(f, p, 1.f / 120.f);
-  p = fmaf(f, p, 1.f / 24.f);
-  p = fmaf(f, p, 1.f / 6.f);
-  p = fmaf(f, p, 0.5f);
-  p = fmaf(f * f, p, f);
-  const float s = gone ? 0.f : __int_as_float((__float_as_int(m) << 23) + 0x3f800000);   // 2^n
-  a = fmaf(s, p, s);
-  const float below = fmaf(-s, p, 1.f - s);      // 1 - a
-  const float z = fmaf(below, a, below);
-  root = z < 1.2e-38f ? 0.f : z * rsqrt_approx(z);
+  y = make_float2(min_nan(y.x, 88.f), min_nan(y.y, 88.f));
+  const F2 m = fma(y, f2(-1.4426950408889634f), f2(kMagic));   // kMagic - n
+  const F2 n = add(m, f2(-kMagic));
+  F2 g = fma(n, f2(0.693147182464599609375f), y);              // ln 2 in two parts
+  g = fma(n, f2(-1.904654290582768e-9f), g);
+  F2 w = fma(g, f2(1.f / 5040.f), f2(-1.f / 720.f));
+  w = fma(g, w, f2(1.f / 120.f));
+  w = fma(g, w, f2(-1.f / 24.f));
+  w = fma(g, w, f2(1.f / 6.f));
+  w = fma(g, w, f2(-0.5f));
+  w = fma(mul(g, g), w, g);
+  const F2 s = make_float2(__int_as_float((__float_as_int(m.x) << 23) + 0x3f800000),
+                           __int_as_float((__float_as_int(m.y) << 23) + 0x3f800000));
+  const F2 ns = make_float2(-s.x, -s.y);
+  a = fma(ns, w, s);
+  const F2 below = fma(s, w, add(ns, f2(1.f)));  // 1 - a
+  const F2 z = fma(below, a, below);
+  root = mul(z, make_float2(rsqrt_approx(fmaxf(z.x, 1.2e-38f)), rsqrt_approx(fmaxf(z.y, 1.2e-38f))));
 }
 
 // ---- sequences and tiles ---------------------------------------------------
@@ -114,12 +130,11 @@ struct Args {
   unsigned* err;
 };
 
-template <int N>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -127,349 +142,400 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <typename T> constexpr int row_bytes() { return kChan * static_cast<int>(sizeof(T)); }
-template <typename T, int MODE> constexpr bool staged() { return MODE != kOdd || sizeof(T) == 4; }
+// Bytes of a staged row, and of a warp's rows of one array.
+template <typename T, int MODE> constexpr int row_bytes() {
+  return kChan * static_cast<int>(sizeof(T)) + (MODE == kOdd && sizeof(T) == 2 ? 4 : 0);
+}
+template <typename T, int MODE> constexpr int run_bytes() {
+  return (kRun * row_bytes<T, MODE>() + 15) / 16 * 16;
+}
 
-// Copies a warp's rows t .. t+7 (those below t1), channels c0 .. c0+63, to `dst`.
+// Copies a warp's rows t .. t+7, channels c0 .. c0+63, to `dst`; rows at or past
+// t1 are filled with `fill` (two bf16, or the float) instead: r = -inf, and zeros
+// elsewhere, make a token the identity.  `total` is the tensor's element count.
 template <typename T, int MODE>
 __device__ __forceinline__ void stage_rows(char* dst, const T* src, int t, int t1, int c0, int D,
-                                           int lane) {
-  if constexpr (staged<T, MODE>()) {
-    constexpr int kPiece = MODE == kWide ? 16 : 4;
-    constexpr int kPer = row_bytes<T>() / kPiece;       // pieces of a row
-    constexpr int kElems = kPiece / static_cast<int>(sizeof(T));
-    const uint32_t d = tc::smem_u32(dst);
+                                           size_t total, uint32_t fill, int lane) {
+  constexpr int kPiece = MODE == kWide ? 16 : 4;
+  constexpr int kRow = row_bytes<T, MODE>();
+  constexpr int kPer = kRow / kPiece;                     // pieces of a row
+  constexpr int kElems = kPiece / static_cast<int>(sizeof(T));
+  const uint32_t d = tc::smem_u32(dst);
 #pragma unroll
-    for (int k = 0; k < kRun * kPer / 32; ++k) {
-      const int idx = k * 32 + lane, row = idx / kPer, p = idx % kPer;
-      if (t + row < t1 && c0 + p * kElems < D)
-        cp_async<kPiece>(d + row * row_bytes<T>() + p * kPiece,
-                         src + static_cast<size_t>(t + row) * D + c0 + p * kElems);
+  for (int k = 0; k < (kRun * kPer + 31) / 32; ++k) {
+    const int idx = k * 32 + lane, row = idx / kPer, p = idx % kPer;
+    if (kRun * kPer % 32 != 0 && row >= kRun) break;
+    const uint32_t to = d + row * kRow + p * kPiece;
+    if (t + row >= t1) {
+      uint32_t* q = reinterpret_cast<uint32_t*>(dst + row * kRow + p * kPiece);
+#pragma unroll
+      for (int n = 0; n < kPiece / 4; ++n) q[n] = fill;
+      continue;
+    }
+    const size_t at = static_cast<size_t>(t + row) * D + c0;
+    if constexpr (MODE == kOdd && sizeof(T) == 2) {
+      const size_t from = (at & ~static_cast<size_t>(1)) + 2 * p;     // even: 4-byte aligned
+      if (from >= at + min(kChan, D - c0)) continue;
+      if (from + 1 < total)
+        cp_async4(to, src + from);
+      else                                                // the tensor's last element
+        *reinterpret_cast<T*>(dst + row * kRow + p * kPiece) = src[from];
+    } else {
+      if (c0 + p * kElems >= D) continue;
+      if constexpr (kPiece == 16)
+        cp_async16(to, src + at + p * kElems);
+      else
+        cp_async4(to, src + at + p * kElems);
     }
   }
 }
 
-// A lane's two channels of row k: from shared memory, or (kOdd bf16) from global.
+// A lane's two channels of staged row k, token t.
 template <typename T, int MODE>
-__device__ __forceinline__ float2 row_pair(const char* st, const T* src, int k, int t, bool okt,
-                                           int cA, int cB, int D, int lane) {
-  if constexpr (!staged<T, MODE>()) {
-    const size_t at = static_cast<size_t>(t) * D;
-    float2 v = make_float2(0.f, 0.f);
-    if (okt && cA < D) v.x = Io<T>::ld(src, at + cA);
-    if (okt && cB < D) v.y = Io<T>::ld(src, at + cB);
-    return v;
+__device__ __forceinline__ F2 row_pair(const char* st, int k, int t, int c0, int D, int lane) {
+  const char* row = st + k * row_bytes<T, MODE>();
+  if constexpr (MODE == kOdd && sizeof(T) == 2) {
+    const unsigned short* q = reinterpret_cast<const unsigned short*>(row) + ((t & D & 1) ^ (c0 & 1));
+    return make_float2(__uint_as_float(static_cast<uint32_t>(q[lane]) << 16),
+                       __uint_as_float(static_cast<uint32_t>(q[lane + 32]) << 16));
   } else if constexpr (sizeof(T) == 2) {
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(st + k * row_bytes<T>() + lane * 4);
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(row + lane * 4);
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
   } else if constexpr (MODE == kOdd) {
-    const float* p = reinterpret_cast<const float*>(st + k * row_bytes<T>());
-    return make_float2(p[lane], p[lane + 32]);
+    const float* q = reinterpret_cast<const float*>(row);
+    return make_float2(q[lane], q[lane + 32]);
   } else {
-    return *reinterpret_cast<const float2*>(st + k * row_bytes<T>() + lane * 8);
+    return *reinterpret_cast<const F2*>(row + lane * 8);
   }
 }
 
+// `at`: offset of the lane's first channel.
 template <typename T, int MODE>
-__device__ __forceinline__ void store_pair(T* dst, int t, float2 v, int cA, int cB, int D) {
-  const size_t at = static_cast<size_t>(t) * D;
+__device__ __forceinline__ void store_pair(T* at, F2 v, bool okA, bool okB) {
   if constexpr (MODE == kOdd) {
-    if (cA < D) Io<T>::st(dst, at + cA, v.x);
-    if (cB < D) Io<T>::st(dst, at + cB, v.y);
-  } else if (cA < D) {
+    if (okA) Io<T>::st(at, 0, v.x);
+    if (okB) Io<T>::st(at, 32, v.y);
+  } else if (okA) {
     if constexpr (sizeof(T) == 2)
-      *reinterpret_cast<__nv_bfloat162*>(dst + at + cA) = __floats2bfloat162_rn(v.x, v.y);
+      *reinterpret_cast<__nv_bfloat162*>(at) = __floats2bfloat162_rn(v.x, v.y);
     else
-      *reinterpret_cast<float2*>(dst + at + cA) = v;
+      *reinterpret_cast<F2*>(at) = v;
   }
 }
 
-__device__ __forceinline__ float2 load2(const float* p, size_t at, int cA, int cB, int D) {
+__device__ __forceinline__ F2 load2(const float* p, size_t at, int cA, int cB, int D) {
   return make_float2(p && cA < D ? p[at + cA] : 0.f, p && cB < D ? p[at + cB] : 0.f);
 }
-__device__ __forceinline__ void store2(float* p, size_t at, float2 v, int cA, int cB, int D) {
+__device__ __forceinline__ void store2(float* p, size_t at, F2 v, int cA, int cB, int D) {
   if (cA < D) p[at + cA] = v.x;
   if (cB < D) p[at + cB] = v.y;
 }
 
-__device__ __forceinline__ void st_cluster_f32x4(uint32_t remote, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(remote), "f"(v.x),
-               "f"(v.y), "f"(v.z), "f"(v.w)
-               : "memory");
-}
+// ---- affine maps and their exchange -------------------------------------------
 
-// Affine maps of a lane's two channels: (A.x, V.x, A.y, V.y).
-__device__ __forceinline__ float2 apply(const float4& m, float2 h) {
-  return make_float2(fmaf(m.x, h.x, m.y), fmaf(m.z, h.y, m.w));
+// h -> A h + V for a lane's two channels.
+struct Map {
+  F2 A, V;
+};
+__device__ __forceinline__ F2 apply(const Map& m, F2 h) { return fma(m.A, h, m.V); }
+__device__ __forceinline__ Map then(const Map& m, const Map& n) {      // first m, then n
+  return Map{mul(n.A, m.A), fma(n.A, m.V, n.V)};
 }
-// first m, then n
-__device__ __forceinline__ float4 then(const float4& m, const float4& n) {
-  return make_float4(n.x * m.x, fmaf(n.x, m.y, n.y), n.z * m.z, fmaf(n.z, m.w, n.w));
-}
+__device__ __forceinline__ Map identity() { return Map{f2(1.f), f2(0.f)}; }
 
-// Maps exchanged in a round, double-buffered by the round's parity: a buffer is
-// written again two rounds later, and every reader has passed the barrier of
-// the round between by then.
 using Maps = float4[32];             // one map per lane
+__device__ __forceinline__ Map get(const Maps& m, int lane) {
+  const float4 v = m[lane];
+  return Map{make_float2(v.x, v.y), make_float2(v.z, v.w)};
+}
+__device__ __forceinline__ float4 pack(const Map& m) {
+  return make_float4(m.A.x, m.A.y, m.V.x, m.V.y);
+}
 
-__host__ __device__ constexpr size_t warp_maps_bytes() { return 2 * kWarps * sizeof(Maps); }
-__host__ __device__ constexpr size_t cta_maps_bytes(int split) {
-  return split > 1 ? 2 * split * sizeof(Maps) : 0;
+// Shared memory of the exchange: per round parity, the maps of the CTA's warps
+// and those of the cluster's CTAs, with a barrier that counts the latter's
+// bytes.  A buffer is written again two rounds later; by then every reader has
+// passed the block barrier (warp maps) of the round between, and a CTA sends its
+// next map only after that, so a map received tells that the sender's warps have
+// read everything of the round before last.
+struct Exchange {
+  Maps warp[2][kWarps];
+  uint64_t bar[2];
+  int abort;
+  int pad[3];
+};
+__host__ __device__ constexpr size_t exchange_bytes(int split) {
+  return sizeof(Exchange) + (split > 1 ? 2 * split * sizeof(Maps) : 0);
+}
+
+__device__ __forceinline__ void st_async_f32x4(uint32_t remote, float4 v, uint32_t remote_bar) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+          remote),
+      "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(remote_bar)
+      : "memory");
+}
+
+// Start of a kernel: every CTA of the cluster is running and its barriers are set up
+// before any map is sent.
+__device__ __forceinline__ void exchange_begin(Exchange& ex, int S) {
+  if (S == 1) return;
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&ex.bar[0], 1);
+    tc::mbar_init(&ex.bar[1], 1);
+    ex.abort = 0;
+    tc::fence_barrier_init();
+  }
+  __syncthreads();
+  tc::cluster_sync();
+}
+// Sends this CTA's map of round `n` to every CTA of the cluster and waits for theirs.  The
+// stores carry their own completion, so nothing here waits for this thread's stores
+// to global memory (a cluster barrier would).  The wait is bounded; once one has run out the
+// others return at once, the rounds go on without exchange and the error is reported.
+__device__ __forceinline__ void exchange(Exchange& ex, Maps* cta, const Map& mine, int n, int S,
+                                         int rank, int warp, int lane, unsigned* err) {
+  Maps* to = cta + (n & 1) * S;
+  uint64_t* bar = &ex.bar[n & 1];
+  if (threadIdx.x == 0 && !*static_cast<volatile int*>(&ex.abort))
+    tc::mbar_arrive_expect_tx(bar, S * sizeof(Maps));
+  for (int q = warp; q < S; q += kWarps)
+    st_async_f32x4(tc::cluster_addr(&to[rank][lane], q), pack(mine), tc::cluster_addr(bar, q));
+  tc::mbar_wait_cluster(bar, (n >> 1) & 1, &ex.abort, err);
 }
 
 // ---- forward ---------------------------------------------------------------
 
 template <typename Ti, typename Th, int MODE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ state_out,
                Th* __restrict__ h, float* __restrict__ chunk_states) {
   extern __shared__ __align__(16) char smem[];
-  constexpr int kArray = kRun * row_bytes<Ti>();        // a warp's rows of one input
+  constexpr int kArray = run_bytes<Ti, MODE>();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int S = p.split;
-  Maps* warp_maps = reinterpret_cast<Maps*>(smem);                       // [2][kWarps]
-  Maps* cta_maps = reinterpret_cast<Maps*>(smem + warp_maps_bytes());    // [2][S]
-  char* ring = smem + warp_maps_bytes() + cta_maps_bytes(S) + warp * (2 * 3 * kArray);
-  const int rank = static_cast<int>(blockIdx.x % S);
+  const int S = p.split, rank = static_cast<int>(blockIdx.x % S);
+  Exchange& ex = *reinterpret_cast<Exchange*>(smem);
+  Maps* cta_maps = reinterpret_cast<Maps*>(smem + sizeof(Exchange));      // [2][S]
+  char* ring = smem + exchange_bytes(S) + warp * (2 * 3 * kArray);
   const int pair = static_cast<int>(blockIdx.x / S);
   const int seq = pair / p.groups, c0 = (pair % p.groups) * kChan;
   const int D = p.D;
   const int cA = c0 + (MODE == kOdd ? lane : 2 * lane), cB = MODE == kOdd ? cA + 32 : cA + 1;
+  const bool okA = cA < D, okB = cB < D;
   const Ti* x = static_cast<const Ti*>(p.x);
   const Ti* r = static_cast<const Ti*>(p.r);
   const Ti* i = static_cast<const Ti*>(p.i);
+  const size_t total = static_cast<size_t>(p.L.Ttot) * D;
   int t0, t1;
   seq_bounds(p.L, seq, t0, t1);
   if (c0 == 0 && rank == 0 && threadIdx.x == 0) check_offsets(p.L, seq, p.err);
   const int rounds = ceil_div(t1 - t0, kTile * S);
+  const uint32_t minus_inf = sizeof(Ti) == 2 ? 0xff80ff80u : 0xff800000u;
   const auto first = [&](int j) { return t0 + ((j * S + rank) * kWarps + warp) * kRun; };
   const auto fetch = [&](int j) {
     char* st = ring + (j & 1) * 3 * kArray;
     if (j < rounds) {
-      stage_rows<Ti, MODE>(st, x, first(j), t1, c0, D, lane);
-      stage_rows<Ti, MODE>(st + kArray, r, first(j), t1, c0, D, lane);
-      stage_rows<Ti, MODE>(st + 2 * kArray, i, first(j), t1, c0, D, lane);
+      const int t = first(j);
+      stage_rows<Ti, MODE>(st, x, t, t1, c0, D, total, 0, lane);
+      stage_rows<Ti, MODE>(st + kArray, r, t, t1, c0, D, total, minus_inf, lane);
+      stage_rows<Ti, MODE>(st + 2 * kArray, i, t, t1, c0, D, total, 0, lane);
     }
     cp_commit();
   };
   fetch(0);
-  const float2 lm = load2(p.lam, 0, cA, cB, D);
-  const float2 ysc = make_float2(p.c * softplus(lm.x), p.c * softplus(lm.y));
-  float2 carry = load2(state_in, static_cast<size_t>(seq) * D, cA, cB, D);
-  if (S > 1) tc::cluster_sync();       // every CTA of the cluster runs before its memory is written
+  const F2 lm = load2(p.lam, 0, cA, cB, D);
+  const F2 ysc = make_float2(p.c * softplus(lm.x), p.c * softplus(lm.y));
+  F2 carry = load2(state_in, static_cast<size_t>(seq) * D, cA, cB, D);
+  exchange_begin(ex, S);
   for (int j = 0; j < rounds; ++j) {
     fetch(j + 1);
     cp_wait<1>();
     __syncwarp();
     const char* st = ring + (j & 1) * 3 * kArray;
     const int t = first(j);
-    float2 a[kRun], v[kRun];
-    float4 m = make_float4(1.f, 0.f, 1.f, 0.f);
+    F2 a[kRun], v[kRun];
+    Map m = identity();
 #pragma unroll
     for (int k = 0; k < kRun; ++k) {
-      const bool ok = t + k < t1;
-      const float2 xv = row_pair<Ti, MODE>(st, x, k, t + k, ok, cA, cB, D, lane);
-      const float2 rv = row_pair<Ti, MODE>(st + kArray, r, k, t + k, ok, cA, cB, D, lane);
-      const float2 iv = row_pair<Ti, MODE>(st + 2 * kArray, i, k, t + k, ok, cA, cB, D, lane);
-      float2 root;
-      decay(ysc.x * sigmoid(rv.x), a[k].x, root.x);
-      decay(ysc.y * sigmoid(rv.y), a[k].y, root.y);
-      v[k] = make_float2(root.x * sigmoid(iv.x) * xv.x, root.y * sigmoid(iv.y) * xv.y);
-      if (!ok) {                          // the identity
-        a[k] = make_float2(1.f, 1.f);
-        v[k] = make_float2(0.f, 0.f);
-      }
-      m = then(m, make_float4(a[k].x, v[k].x, a[k].y, v[k].y));
+      const F2 xv = row_pair<Ti, MODE>(st, k, t + k, c0, D, lane);
+      const F2 rv = row_pair<Ti, MODE>(st + kArray, k, t + k, c0, D, lane);
+      const F2 iv = row_pair<Ti, MODE>(st + 2 * kArray, k, t + k, c0, D, lane);
+      F2 root;
+      decay(mul(ysc, sigmoid(rv)), a[k], root);
+      v[k] = mul(mul(root, sigmoid(iv)), xv);
+      m = then(m, Map{a[k], v[k]});
     }
-    Maps* wm = warp_maps + (j & 1) * kWarps;
-    wm[warp][lane] = m;
+    Maps* wm = ex.warp[j & 1];
+    wm[warp][lane] = pack(m);
     __syncthreads();
-    float4 before = make_float4(1.f, 0.f, 1.f, 0.f), total = before;
+    Map before = identity(), all = before;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (w == warp) before = total;
-      total = then(total, wm[w][lane]);
+      if (w == warp) before = all;
+      all = then(all, get(wm[w], lane));
     }
-    float2 enter = carry;
+    F2 enter = carry;
     if (S > 1) {
+      exchange(ex, cta_maps, all, j, S, rank, warp, lane, p.err);
       Maps* cm = cta_maps + (j & 1) * S;
-      for (int q = warp; q < S; q += kWarps)
-        st_cluster_f32x4(tc::cluster_addr(&cm[rank][lane], q), total);
-      tc::cluster_sync();
       for (int q = 0; q < S; ++q) {
         if (q == rank) enter = carry;
-        carry = apply(cm[q][lane], carry);
+        carry = apply(get(cm[q], lane), carry);
       }
     } else {
-      carry = apply(total, carry);
+      carry = apply(all, carry);
     }
-    const int tile = j * S + rank;
     if (chunk_states && warp == 0 && t < t1)
-      store2(chunk_states, static_cast<size_t>(chunk_row(t0, seq) + tile) * D, enter, cA, cB, D);
-    float2 hs = apply(before, enter);
+      store2(chunk_states, static_cast<size_t>(chunk_row(t0, seq) + j * S + rank) * D, enter, cA,
+             cB, D);
+    F2 hs = apply(before, enter);
+    Th* out = h + static_cast<size_t>(t) * D + cA;
 #pragma unroll
     for (int k = 0; k < kRun; ++k) {
-      hs = make_float2(fmaf(a[k].x, hs.x, v[k].x), fmaf(a[k].y, hs.y, v[k].y));
-      if (t + k < t1) store_pair<Th, MODE>(h, t + k, hs, cA, cB, D);
+      hs = fma(a[k], hs, v[k]);
+      if (t + k < t1) store_pair<Th, MODE>(out, hs, okA, okB);
+      out += D;
     }
   }
   if (state_out && rank == 0 && warp == 0)
     store2(state_out, static_cast<size_t>(seq) * D, carry, cA, cB, D);
+  if (S > 1) tc::cluster_sync();       // no CTA leaves while maps may still be on their way to it
 }
 
 // ---- gradients -------------------------------------------------------------
 
 template <typename Ti, typename Tu, typename Tg, int MODE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restrict__ dh,
                const float* __restrict__ d_state_out, Tg* __restrict__ dx, Tg* __restrict__ dr,
                Tg* __restrict__ di, float* __restrict__ d_state_in, float* __restrict__ partial) {
   extern __shared__ __align__(16) char smem[];
-  constexpr int kArray = kRun * row_bytes<Ti>(), kUp = kRun * row_bytes<Tu>();
+  constexpr int kArray = run_bytes<Ti, MODE>(), kUp = run_bytes<Tu, MODE>();
   constexpr int kStage = 3 * kArray + kUp;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int S = p.split;
-  Maps* warp_maps = reinterpret_cast<Maps*>(smem);                       // [2][kWarps]
-  Maps* cta_maps = reinterpret_cast<Maps*>(smem + warp_maps_bytes());    // [2][S]
-  float2(*wf)[kWarps][32] = reinterpret_cast<float2(*)[kWarps][32]>(
-      smem + warp_maps_bytes() + cta_maps_bytes(S));
+  const int S = p.split, rank = static_cast<int>(blockIdx.x % S);
+  Exchange& ex = *reinterpret_cast<Exchange*>(smem);
+  Maps* cta_maps = reinterpret_cast<Maps*>(smem + sizeof(Exchange));      // [2][S]
+  F2(*wf)[kWarps][32] = reinterpret_cast<F2(*)[kWarps][32]>(smem + exchange_bytes(S));
   char* ring = reinterpret_cast<char*>(wf + 2) + warp * (2 * kStage);
-  const int rank = static_cast<int>(blockIdx.x % S);
   const int pair = static_cast<int>(blockIdx.x / S);
   const int seq = pair / p.groups, c0 = (pair % p.groups) * kChan;
   const int D = p.D;
   const int cA = c0 + (MODE == kOdd ? lane : 2 * lane), cB = MODE == kOdd ? cA + 32 : cA + 1;
+  const bool okA = cA < D, okB = cB < D;
   const Ti* x = static_cast<const Ti*>(p.x);
   const Ti* r = static_cast<const Ti*>(p.r);
   const Ti* i = static_cast<const Ti*>(p.i);
+  const size_t total = static_cast<size_t>(p.L.Ttot) * D;
   int t0, t1;
   seq_bounds(p.L, seq, t0, t1);
   if (c0 == 0 && rank == 0 && threadIdx.x == 0) check_offsets(p.L, seq, p.err);
   const int rounds = ceil_div(t1 - t0, kTile * S);
+  const uint32_t minus_inf = sizeof(Ti) == 2 ? 0xff80ff80u : 0xff800000u;
   const auto first = [&](int j) { return t0 + ((j * S + rank) * kWarps + warp) * kRun; };
   const auto fetch = [&](int j) {
     char* st = ring + (j & 1) * kStage;
     if (j >= 0) {
-      stage_rows<Ti, MODE>(st, x, first(j), t1, c0, D, lane);
-      stage_rows<Ti, MODE>(st + kArray, r, first(j), t1, c0, D, lane);
-      stage_rows<Ti, MODE>(st + 2 * kArray, i, first(j), t1, c0, D, lane);
-      stage_rows<Tu, MODE>(st + 3 * kArray, dh, first(j), t1, c0, D, lane);
+      const int t = first(j);
+      stage_rows<Ti, MODE>(st, x, t, t1, c0, D, total, 0, lane);
+      stage_rows<Ti, MODE>(st + kArray, r, t, t1, c0, D, total, minus_inf, lane);
+      stage_rows<Ti, MODE>(st + 2 * kArray, i, t, t1, c0, D, total, 0, lane);
+      stage_rows<Tu, MODE>(st + 3 * kArray, dh, t, t1, c0, D, total, 0, lane);
     }
     cp_commit();
   };
   const auto entering = [&](int j) {
     const int tile = j * S + rank;
-    if (j < 0 || t0 + tile * kTile >= t1) return make_float2(0.f, 0.f);
+    if (j < 0 || t0 + tile * kTile >= t1) return f2(0.f);
     return load2(chunk_states, static_cast<size_t>(chunk_row(t0, seq) + tile) * D, cA, cB, D);
   };
   fetch(rounds - 1);
-  float2 cs = entering(rounds - 1);
-  const float2 lm = load2(p.lam, 0, cA, cB, D);
-  const float2 ysc = make_float2(p.c * softplus(lm.x), p.c * softplus(lm.y));
+  F2 cs = entering(rounds - 1);
+  const F2 lm = load2(p.lam, 0, cA, cB, D);
+  const F2 ysc = make_float2(p.c * softplus(lm.x), p.c * softplus(lm.y));
   const size_t so = static_cast<size_t>(seq) * D;
-  float2 carry = load2(d_state_out, so, cA, cB, D);
-  float2 usum = make_float2(0.f, 0.f);
-  if (S > 1) tc::cluster_sync();
+  F2 carry = load2(d_state_out, so, cA, cB, D);
+  F2 usum = f2(0.f);
+  exchange_begin(ex, S);
   for (int j = rounds - 1; j >= 0; --j) {
+    const int n = rounds - 1 - j;
     __syncwarp();                         // the buffer refilled now was read to the round's end
     fetch(j - 1);
-    const float2 cs_next = entering(j - 1);
+    const F2 cs_next = entering(j - 1);
     cp_wait<1>();
     __syncwarp();
     const char* st = ring + (j & 1) * kStage;
     const int t = first(j);
-    // the run's map of h forwards (product in fw, sum below) and of e backwards
-    float2 a[kRun], root[kRun], sr[kRun], si[kRun];
-    float4 fw = make_float4(1.f, 0.f, 1.f, 0.f);
+    // the run's map of h forwards (fw) and of e backwards (the same product, sum w)
+    F2 a[kRun], root[kRun], sr[kRun], si[kRun];
+    Map fw = identity();
 #pragma unroll
     for (int k = 0; k < kRun; ++k) {
-      const bool ok = t + k < t1;
-      const float2 xv = row_pair<Ti, MODE>(st, x, k, t + k, ok, cA, cB, D, lane);
-      const float2 rv = row_pair<Ti, MODE>(st + kArray, r, k, t + k, ok, cA, cB, D, lane);
-      const float2 iv = row_pair<Ti, MODE>(st + 2 * kArray, i, k, t + k, ok, cA, cB, D, lane);
-      sr[k] = make_float2(sigmoid(rv.x), sigmoid(rv.y));
-      si[k] = make_float2(sigmoid(iv.x), sigmoid(iv.y));
-      decay(ysc.x * sr[k].x, a[k].x, root[k].x);
-      decay(ysc.y * sr[k].y, a[k].y, root[k].y);
-      float2 v = make_float2(root[k].x * si[k].x * xv.x, root[k].y * si[k].y * xv.y);
-      if (!ok) {                          // the identity
-        a[k] = make_float2(1.f, 1.f);
-        v = make_float2(0.f, 0.f);
-      }
-      fw = then(fw, make_float4(a[k].x, v.x, a[k].y, v.y));
+      const F2 xv = row_pair<Ti, MODE>(st, k, t + k, c0, D, lane);
+      const F2 rv = row_pair<Ti, MODE>(st + kArray, k, t + k, c0, D, lane);
+      const F2 iv = row_pair<Ti, MODE>(st + 2 * kArray, k, t + k, c0, D, lane);
+      sr[k] = sigmoid(rv);
+      si[k] = sigmoid(iv);
+      decay(mul(ysc, sr[k]), a[k], root[k]);
+      fw = then(fw, Map{a[k], mul(mul(root[k], si[k]), xv)});
     }
-    float2 w = make_float2(0.f, 0.f);
+    F2 w = f2(0.f);
 #pragma unroll
-    for (int k = kRun - 1; k >= 0; --k) {
-      const bool ok = t + k < t1;
-      const float2 u = row_pair<Tu, MODE>(st + 3 * kArray, dh, k, t + k, ok, cA, cB, D, lane);
-      if (ok)
-        w = make_float2(a[k].x * (u.x + w.x), a[k].y * (u.y + w.y));
-    }
-    Maps* wm = warp_maps + (j & 1) * kWarps;
-    wm[warp][lane] = make_float4(fw.x, w.x, fw.z, w.y);
-    wf[j & 1][warp][lane] = make_float2(fw.y, fw.w);
+    for (int k = kRun - 1; k >= 0; --k)
+      w = mul(a[k], add(row_pair<Tu, MODE>(st + 3 * kArray, k, t + k, c0, D, lane), w));
+    Maps* wm = ex.warp[n & 1];
+    wm[warp][lane] = pack(Map{fw.A, w});
+    wf[n & 1][warp][lane] = fw.V;
     __syncthreads();
-    float2 hs = cs;                       // the state that enters this warp's run
-    for (int q = 0; q < warp; ++q) {
-      const float4 mq = wm[q][lane];
-      const float2 vq = wf[j & 1][q][lane];
-      hs = make_float2(fmaf(mq.x, hs.x, vq.x), fmaf(mq.z, hs.y, vq.y));
-    }
-    float4 after = make_float4(1.f, 0.f, 1.f, 0.f), total = after;
+    F2 hs = cs;                           // the state that enters this warp's run
+    for (int q = 0; q < warp; ++q) hs = fma(get(wm[q], lane).A, hs, wf[n & 1][q][lane]);
+    Map after = identity(), all = after;
 #pragma unroll
     for (int q = kWarps - 1; q >= 0; --q) {
-      if (q == warp) after = total;
-      total = then(total, wm[q][lane]);
+      if (q == warp) after = all;
+      all = then(all, get(wm[q], lane));
     }
-    float2 e = carry;
+    F2 e = carry;
     if (S > 1) {
-      Maps* cm = cta_maps + (j & 1) * S;
-      for (int q = warp; q < S; q += kWarps)
-        st_cluster_f32x4(tc::cluster_addr(&cm[rank][lane], q), total);
-      tc::cluster_sync();
+      exchange(ex, cta_maps, all, n, S, rank, warp, lane, p.err);
+      Maps* cm = cta_maps + (n & 1) * S;
       for (int q = S - 1; q >= 0; --q) {
         if (q == rank) e = carry;
-        carry = apply(cm[q][lane], carry);
+        carry = apply(get(cm[q], lane), carry);
       }
     } else {
-      carry = apply(total, carry);
+      carry = apply(all, carry);
     }
     e = apply(after, e);
-    float2 hp[kRun];                      // the state before each token
+    F2 hp[kRun];                          // the state before each token
 #pragma unroll
     for (int k = 0; k < kRun; ++k) {
       hp[k] = hs;
-      const bool ok = t + k < t1;
-      const float2 xv = row_pair<Ti, MODE>(st, x, k, t + k, ok, cA, cB, D, lane);
-      if (ok)
-        hs = make_float2(fmaf(a[k].x, hs.x, root[k].x * si[k].x * xv.x),
-                         fmaf(a[k].y, hs.y, root[k].y * si[k].y * xv.y));
+      const F2 xv = row_pair<Ti, MODE>(st, k, t + k, c0, D, lane);
+      hs = fma(a[k], hs, mul(mul(root[k], si[k]), xv));
     }
+    const size_t at = static_cast<size_t>(t) * D + cA;
 #pragma unroll
     for (int k = kRun - 1; k >= 0; --k) {
-      const bool ok = t + k < t1;
-      if (!ok) continue;
-      const float2 xv = row_pair<Ti, MODE>(st, x, k, t + k, ok, cA, cB, D, lane);
-      const float2 uv = row_pair<Tu, MODE>(st + 3 * kArray, dh, k, t + k, ok, cA, cB, D, lane);
-      float2 gx, gi, gr;
-      const auto one = [](float a, float root, float sr, float si, float ysc, float x, float dh,
-                          float hp, float& e, float& usum, float& gx, float& gr, float& gi) {
-        const float G = dh + e, inv = root > 0.f ? rcp_approx(root) : 0.f;
-        gx = G * (root * si);
-        gi = gx * x * (1.f - si);
-        const float u = G * a * (ysc * sr) * fmaf(a * inv, si * x, -hp);
-        gr = u * (1.f - sr);
-        usum += u;
-        e = a * G;
-      };
-      one(a[k].x, root[k].x, sr[k].x, si[k].x, ysc.x, xv.x, uv.x, hp[k].x, e.x, usum.x, gx.x, gr.x,
-          gi.x);
-      one(a[k].y, root[k].y, sr[k].y, si[k].y, ysc.y, xv.y, uv.y, hp[k].y, e.y, usum.y, gx.y, gr.y,
-          gi.y);
-      store_pair<Tg, MODE>(dx, t + k, gx, cA, cB, D);
-      store_pair<Tg, MODE>(dr, t + k, gr, cA, cB, D);
-      store_pair<Tg, MODE>(di, t + k, gi, cA, cB, D);
+      const F2 xv = row_pair<Ti, MODE>(st, k, t + k, c0, D, lane);
+      const F2 G = add(row_pair<Tu, MODE>(st + 3 * kArray, k, t + k, c0, D, lane), e);
+      // 1 / root, or zero at a decay of one, where y / root tends to zero
+      const F2 inv = make_float2(root[k].x > 0.f ? rcp_approx(root[k].x) : 0.f,
+                                 root[k].y > 0.f ? rcp_approx(root[k].y) : 0.f);
+      const F2 minus = f2(-1.f);
+      const F2 six = mul(si[k], xv);
+      const F2 gx = mul(G, mul(root[k], si[k]));
+      const F2 gi = mul(mul(gx, xv), fma(si[k], minus, f2(1.f)));
+      e = mul(a[k], G);
+      const F2 u = mul(mul(e, mul(ysc, sr[k])), fma(mul(a[k], inv), six, mul(hp[k], minus)));
+      const F2 gr = mul(u, fma(sr[k], minus, f2(1.f)));
+      usum = add(usum, u);
+      if (t + k < t1) {
+        const size_t o = at + static_cast<size_t>(k) * D;
+        store_pair<Tg, MODE>(dx + o, gx, okA, okB);
+        store_pair<Tg, MODE>(dr + o, gr, okA, okB);
+        store_pair<Tg, MODE>(di + o, gi, okA, okB);
+      }
     }
     cs = cs_next;
   }
@@ -480,12 +546,10 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
   __syncthreads();
   if (warp == 0) {
 #pragma unroll
-    for (int q = 1; q < kWarps; ++q) {
-      usum.x += wf[0][q][lane].x;
-      usum.y += wf[0][q][lane].y;
-    }
+    for (int q = 1; q < kWarps; ++q) usum = add(usum, wf[0][q][lane]);
     store2(partial, (static_cast<size_t>(seq) * S + rank) * D, usum, cA, cB, D);
   }
+  if (S > 1) tc::cluster_sync();       // no CTA leaves while maps may still be on their way to it
 }
 
 // d_lam = (sum of the partial rows) sigmoid(lam) / softplus(lam).  32 channels
@@ -518,10 +582,11 @@ glr_step_kernel(const Ti* __restrict__ x, const Ti* __restrict__ r, const Ti* __
   const int d = (blockIdx.x % groups) * 128 + threadIdx.x;
   if (d >= D) return;
   const size_t at = static_cast<size_t>(blockIdx.x / groups) * D + d;
-  float a, root;
-  decay(c * softplus(lam[d]) * sigmoid(Io<Ti>::ld(r, at)), a, root);
-  const float v = root * sigmoid(Io<Ti>::ld(i, at)) * Io<Ti>::ld(x, at);
-  const float st = fmaf(a, state[at], v);
+  // one channel: the decay in the pair's first half, the input gate in the sigmoids' second
+  const F2 s = sigmoid(make_float2(Io<Ti>::ld(r, at), Io<Ti>::ld(i, at)));
+  F2 a, root;
+  decay(f2(c * softplus(lam[d]) * s.x), a, root);
+  const float st = fmaf(a.x, state[at], root.x * s.y * Io<Ti>::ld(x, at));
   state_out[at] = st;
   if (h) Io<Th>::st(h, at, st);
 }
@@ -560,7 +625,7 @@ int split_of(int nseq, long long Ttot, int D, int resident) {
   }
   return best;
 }
-constexpr int kFwdResident = 3 * 148, kBwdResident = 1 * 148;
+constexpr int kFwdResident = 3 * 148, kBwdResident = 2 * 148;
 
 // Fills the common arguments and launches `kern` on clusters of `split` CTAs.
 template <typename... P, typename... A>
@@ -608,9 +673,7 @@ cudaError_t launch_glr_fwd(const void* x, const void* r, const void* i, DType in
         using Ti = decltype(ti);
         using Th = decltype(th);
         constexpr int M = decltype(mode)::value;
-        const size_t smem =
-            warp_maps_bytes() + cta_maps_bytes(p.split) +
-            (staged<Ti, M>() ? 2 * 3 * kTile * row_bytes<Ti>() : 0);
+        const size_t smem = exchange_bytes(p.split) + 2 * 3 * kWarps * run_bytes<Ti, M>();
         return launch_split(glr_fwd_kernel<Ti, Th, M>, smem, blocks, p.split, s, p, state_in,
                             state_out, static_cast<Th*>(h), chunk_states);
       });
@@ -635,9 +698,9 @@ cudaError_t launch_glr_bwd(const void* x, const void* r, const void* i, DType in
           using Tu = decltype(tu);
           using Tg = decltype(tg);
           constexpr int M = decltype(mode)::value;
-          const size_t smem = warp_maps_bytes() + cta_maps_bytes(p.split) +
-                              2 * kWarps * 32 * sizeof(float2) +
-                              2 * kTile * (3 * row_bytes<Ti>() + row_bytes<Tu>());
+          const size_t smem =
+              exchange_bytes(p.split) + 2 * kWarps * 32 * sizeof(F2) +
+              2 * kWarps * (3 * run_bytes<Ti, M>() + run_bytes<Tu, M>());
           return launch_split(glr_bwd_kernel<Ti, Tu, Tg, M>, smem, blocks, p.split, s, p,
                               chunk_states, static_cast<const Tu*>(d_h), d_state_out,
                               static_cast<Tg*>(dx), static_cast<Tg*>(dr), static_cast<Tg*>(di),
