@@ -795,7 +795,7 @@ ret_status retention_glr_fwd(const void* x, const void* r, const void* i, ret_dt
 size_t retention_glr_bwd_workspace_size(int B, int T, int D, int nseq) {
   ret::SeqLayout L;
   if (glr_layout(B, T, D, nullptr, nseq, &L) != RET_OK) return 0;
-  return round256(static_cast<size_t>(ret::glr_bwd_partial_rows(L.nseq, L.Ttot, D)) * D *
+  return round256(static_cast<size_t>(ret::glr_bwd_partial_rows(L, D)) * D *
                   sizeof(float));
 }
 

@@ -17,6 +17,7 @@
 //
 // The inputs of the next round are copied to shared memory (cp.async) while the
 // current one is computed.
+#include <cmath>
 #include <type_traits>
 
 #include "launch.h"
@@ -26,11 +27,12 @@ namespace ret {
 namespace {
 
 constexpr int kTile = kGlrChunk;    // tokens of a CTA per round
-constexpr int kWarps = 8;
-constexpr int kRun = kTile / kWarps;   // tokens of a warp
 constexpr int kChan = 64;           // channels of a CTA: two per lane
-constexpr int kThreads = kWarps * 32;
 constexpr int kMaxSplit = 16;       // CTAs of a cluster
+// Warps of a CTA, and the consecutive tokens (run) of each.  Long runs share the cost of
+// a round's exchange; the gradients keep three times as much per token in registers.
+constexpr int kFwdWarps = 4, kFwdRun = kTile / kFwdWarps;
+constexpr int kBwdWarps = 8, kBwdRun = kTile / kBwdWarps;
 
 // How a lane's two channels lie and how rows reach shared memory.
 //   kWide: channels 2l, 2l+1; rows are copied in 16-byte pieces (D e bytes divide by 16)
@@ -72,6 +74,7 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
+
 __device__ __forceinline__ F2 sigmoid(F2 x) {
   const F2 n = mul(x, f2(-1.4426950408889634f));
   const F2 d = add(make_float2(ex2_approx(n.x), ex2_approx(n.y)), f2(1.f));
@@ -79,8 +82,9 @@ __device__ __forceinline__ F2 sigmoid(F2 x) {
 }
 
 // a = exp(-y) and root = sqrt(1 - a^2) for y >= 0, both to a few units of their
-// own last place.  y = n ln 2 + g, |g| <= ln 2 / 2, and with w = 1 - e^-g (Taylor;
-// the eighth term is below 2^-25 of the first) a = 2^-n - 2^-n w and
+// own last place.  y = n ln 2 + g, |g| <= ln 2 / 2, and with w = 1 - e^-g = g + g^2 q(g)
+// (q: the degree-4 polynomial of least largest error, found by reweighted least squares
+// on Chebyshev points; w is off by a quarter of 2^-24) a = 2^-n - 2^-n w and
 // 1 - a = 1 - 2^-n + 2^-n w, so 1 - a^2 = (1 - a)(1 + a) cancels nothing for decays
 // near one.  From n = 127 on (y above 87.7, a below 8e-39) 2^-n is taken as zero,
 // and root is zero where 1 - a^2 is below the normal range.
@@ -99,10 +103,9 @@ __device__ __forceinline__ void decay(F2 y, F2& a, F2& root) {
     s = make_float2(__int_as_float((__float_as_int(m.x) << 23) + 0x3f800000),
                     __int_as_float((__float_as_int(m.y) << 23) + 0x3f800000));
   }
-  F2 w = fma(g, f2(1.f / 5040.f), f2(-1.f / 720.f));
-  w = fma(g, w, f2(1.f / 120.f));
-  w = fma(g, w, f2(-1.f / 24.f));
-  w = fma(g, w, f2(1.f / 6.f));
+  F2 w = fma(g, f2(-0.0013945651007816195f), f2(0.008366155438125134f));
+  w = fma(g, w, f2(-0.04166629537940025f));
+  w = fma(g, w, f2(0.1666654795408249f));
   w = fma(g, w, f2(-0.5f));
   w = fma(mul(g, g), w, g);
   F2 below = w;                                    // 1 - a
@@ -157,14 +160,14 @@ __device__ __forceinline__ void cp_wait() {
 template <typename T, int MODE> constexpr int row_bytes() {
   return kChan * static_cast<int>(sizeof(T)) + (MODE == kOdd && sizeof(T) == 2 ? 4 : 0);
 }
-template <typename T, int MODE> constexpr int run_bytes() {
-  return (kRun * row_bytes<T, MODE>() + 15) / 16 * 16;
+template <typename T, int MODE, int RUN> constexpr int run_bytes() {
+  return (RUN * row_bytes<T, MODE>() + 15) / 16 * 16;
 }
 
 // Copies a warp's rows t .. t+7, channels c0 .. c0+63, to `dst`; rows at or past
 // t1 are filled with `fill` (two bf16, or the float) instead: r = -inf, and zeros
 // elsewhere, make a token the identity.  `total` is the tensor's element count.
-template <typename T, int MODE>
+template <typename T, int MODE, int RUN>
 __device__ __forceinline__ void stage_rows(char* dst, const T* src, int t, int t1, int c0, int D,
                                            size_t total, uint32_t fill, int lane) {
   constexpr int kPiece = MODE == kWide ? 16 : 4;
@@ -173,9 +176,9 @@ __device__ __forceinline__ void stage_rows(char* dst, const T* src, int t, int t
   constexpr int kElems = kPiece / static_cast<int>(sizeof(T));
   const uint32_t d = tc::smem_u32(dst);
 #pragma unroll
-  for (int k = 0; k < (kRun * kPer + 31) / 32; ++k) {
+  for (int k = 0; k < (RUN * kPer + 31) / 32; ++k) {
     const int idx = k * 32 + lane, row = idx / kPer, p = idx % kPer;
-    if (kRun * kPer % 32 != 0 && row >= kRun) break;
+    if (RUN * kPer % 32 != 0 && row >= RUN) break;
     const uint32_t to = d + row * kRow + p * kPiece;
     if (t + row >= t1) {
       uint32_t* q = reinterpret_cast<uint32_t*>(dst + row * kRow + p * kPiece);
@@ -210,7 +213,7 @@ __device__ __forceinline__ const T* stage_from(const T* src, int t, int c0, int 
   const int row = kPer < 32 ? lane / kPer : 0, p = kPer < 32 ? lane % kPer : lane;
   return src + static_cast<ptrdiff_t>(t + row) * D + c0 + p * kElems;
 }
-template <typename T, int MODE>
+template <typename T, int MODE, int RUN>
 __device__ __forceinline__ void stage_full(char* dst, const T* from, int c0, int D, int lane) {
   constexpr int kPiece = MODE == kWide ? 16 : 4;
   constexpr int kPer = row_bytes<T, MODE>() / kPiece;
@@ -220,7 +223,7 @@ __device__ __forceinline__ void stage_full(char* dst, const T* from, int c0, int
     constexpr int kStep = 32 / kPer;                      // rows per copy of the warp
     if (c0 + (lane % kPer) * kElems >= D) return;
 #pragma unroll
-    for (int k = 0; k < kRun / kStep; ++k) {
+    for (int k = 0; k < RUN / kStep; ++k) {
       if constexpr (kPiece == 16)
         cp_async16(d + k * 32 * kPiece, from + static_cast<ptrdiff_t>(k * kStep) * D);
       else
@@ -229,20 +232,20 @@ __device__ __forceinline__ void stage_full(char* dst, const T* from, int c0, int
   } else {                                                // float32 in 4-byte pieces: two per row
     const bool okA = c0 + lane < D, okB = c0 + 32 + lane < D;
 #pragma unroll
-    for (int k = 0; k < kRun; ++k) {
+    for (int k = 0; k < RUN; ++k) {
       if (okA) cp_async4(d + k * 256, from + static_cast<ptrdiff_t>(k) * D);
       if (okB) cp_async4(d + k * 256 + 128, from + static_cast<ptrdiff_t>(k) * D + 32);
     }
   }
 }
 // One warp's rows of one array, by whichever way fits.
-template <typename T, int MODE>
+template <typename T, int MODE, int RUN>
 __device__ __forceinline__ void stage(char* dst, const T* src, const T* from, int t, int t1, int c0,
                                       int D, size_t total, uint32_t fill, int lane) {
-  if ((MODE != kOdd || sizeof(T) == 4) && t + kRun <= t1)
-    stage_full<T, MODE>(dst, from, c0, D, lane);
+  if ((MODE != kOdd || sizeof(T) == 4) && t + RUN <= t1)
+    stage_full<T, MODE, RUN>(dst, from, c0, D, lane);
   else
-    stage_rows<T, MODE>(dst, src, t, t1, c0, D, total, fill, lane);
+    stage_rows<T, MODE, RUN>(dst, src, t, t1, c0, D, total, fill, lane);
 }
 
 // A lane's two channels of staged row k, token t.
@@ -314,7 +317,7 @@ __device__ __forceinline__ float4 pack(const Map& m) {
 // next map only after that, so a map received tells that the sender's warps have
 // read everything of the round before last.
 struct Exchange {
-  Maps warp[2][kWarps];
+  Maps warp[2][8];
   uint64_t bar[2];
   int abort;
   int pad[3];
@@ -372,11 +375,12 @@ __device__ __forceinline__ void receive(Exchange& ex, int n, unsigned* err) {
 // ---- forward ---------------------------------------------------------------
 
 template <typename Ti, typename Th, int MODE>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kFwdWarps * 32, 4)
 glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ state_out,
                Th* __restrict__ h, float* __restrict__ chunk_states) {
   extern __shared__ __align__(16) char smem[];
-  constexpr int kArray = run_bytes<Ti, MODE>();
+  constexpr int kWarps = kFwdWarps, kRun = kFwdRun;
+  constexpr int kArray = run_bytes<Ti, MODE, kRun>();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int S = p.split, rank = static_cast<int>(blockIdx.x % S);
   Exchange& ex = *reinterpret_cast<Exchange*>(smem);
@@ -405,9 +409,9 @@ glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ s
     char* st = ring + (j & 1) * 3 * kArray;
     if (j < rounds) {
       const int t = first(j);
-      stage<Ti, MODE>(st, x, xp, t, t1, c0, D, total, 0, lane);
-      stage<Ti, MODE>(st + kArray, r, rp, t, t1, c0, D, total, minus_inf, lane);
-      stage<Ti, MODE>(st + 2 * kArray, i, ip, t, t1, c0, D, total, 0, lane);
+      stage<Ti, MODE, kRun>(st, x, xp, t, t1, c0, D, total, 0, lane);
+      stage<Ti, MODE, kRun>(st + kArray, r, rp, t, t1, c0, D, total, minus_inf, lane);
+      stage<Ti, MODE, kRun>(st + 2 * kArray, i, ip, t, t1, c0, D, total, 0, lane);
       xp += stride;
       rp += stride;
       ip += stride;
@@ -458,8 +462,10 @@ glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ s
         receive(ex, j, p.err);
         const Maps* cm = cta_maps + (j & 1) * S;
         int q = 0;
+#pragma unroll 4
         for (; q < rank; ++q) carry = apply(get(cm[q], lane), carry);
         enter = carry;
+#pragma unroll 4
         for (; q < S; ++q) carry = apply(get(cm[q], lane), carry);
         hs = apply(before, enter);
       }
@@ -495,12 +501,13 @@ glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ s
 // ---- gradients -------------------------------------------------------------
 
 template <typename Ti, typename Tu, typename Tg, int MODE>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kBwdWarps * 32, 2)
 glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restrict__ dh,
                const float* __restrict__ d_state_out, Tg* __restrict__ dx, Tg* __restrict__ dr,
                Tg* __restrict__ di, float* __restrict__ d_state_in, float* __restrict__ partial) {
   extern __shared__ __align__(16) char smem[];
-  constexpr int kArray = run_bytes<Ti, MODE>(), kUp = run_bytes<Tu, MODE>();
+  constexpr int kWarps = kBwdWarps, kRun = kBwdRun;
+  constexpr int kArray = run_bytes<Ti, MODE, kRun>(), kUp = run_bytes<Tu, MODE, kRun>();
   constexpr int kStage = 3 * kArray + kUp;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int S = p.split, rank = static_cast<int>(blockIdx.x % S);
@@ -533,10 +540,10 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
     char* st = ring + (j & 1) * kStage;
     if (j >= 0) {
       const int t = first(j);
-      stage<Ti, MODE>(st, x, xp, t, t1, c0, D, total, 0, lane);
-      stage<Ti, MODE>(st + kArray, r, rp, t, t1, c0, D, total, minus_inf, lane);
-      stage<Ti, MODE>(st + 2 * kArray, i, ip, t, t1, c0, D, total, 0, lane);
-      stage<Tu, MODE>(st + 3 * kArray, dh, up, t, t1, c0, D, total, 0, lane);
+      stage<Ti, MODE, kRun>(st, x, xp, t, t1, c0, D, total, 0, lane);
+      stage<Ti, MODE, kRun>(st + kArray, r, rp, t, t1, c0, D, total, minus_inf, lane);
+      stage<Ti, MODE, kRun>(st + 2 * kArray, i, ip, t, t1, c0, D, total, 0, lane);
+      stage<Tu, MODE, kRun>(st + 3 * kArray, dh, up, t, t1, c0, D, total, 0, lane);
       xp -= stride;
       rp -= stride;
       ip -= stride;
@@ -609,8 +616,10 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
         receive(ex, n, p.err);
         const Maps* cm = cta_maps + (n & 1) * S;
         int q = S - 1;
+#pragma unroll 4
         for (; q > rank; --q) carry = apply(get(cm[q], lane), carry);
         e = apply(after, carry);
+#pragma unroll 4
         for (; q >= 0; --q) carry = apply(get(cm[q], lane), carry);
       }
       F2 hp[kRun];                        // the state before each token
@@ -717,31 +726,43 @@ cudaError_t by_mode(DType in_t, int D, F&& f) {
   return f(std::integral_constant<int, kOdd>{});
 }
 
-// CTAs per cluster: the split of time that ends first when `resident` CTAs run
-// at once, each round taking the same time.
-int split_of(int nseq, long long Ttot, int D, int resident) {
-#ifdef GLR_SPLIT
-  return GLR_SPLIT;
-#endif
-  const long long pairs = static_cast<long long>((D + kChan - 1) / kChan) * nseq;
-  const long long tiles = (Ttot + static_cast<long long>(nseq) * kTile - 1) / (static_cast<long long>(nseq) * kTile);
+// CTAs per cluster.  The busiest SM takes ceil(CTAs / SMs) of them (more than fit at once
+// follow one another), each ceil(tiles / S) rounds and about one more to start and end; a
+// round grows by ~4 % with each CTA whose map it waits for, an SM with a single CTA has
+// nothing to run meanwhile, and large clusters whose CTAs share SMs are slow.  Measured in
+// ms, forward / gradients: at 2 x 8192 x 4096 bf16 S = 1: 0.178/0.442, 2: 0.140/0.309, 6: 0.138/0.351,
+// 16: 0.173/0.433; at 1 x 16384 x 1024 S = 4: 0.119/0.242, 12: 0.060/0.124, 16: 0.058/0.158.
+// Packed sequences differ in length: the SMs share the average and the longest, taken as four
+// times the average, ends last (64 sequences, 200000 tokens x 1024: S = 1: 0.581, 4: 0.440,
+// 16: 0.625).
+int split_of(const SeqLayout& L, int D) {
+  constexpr double kSms = 148.0;
+  const double pairs = static_cast<double>((D + kChan - 1) / kChan) * L.nseq;
+  const long long per = static_cast<long long>(L.nseq) * kTile;
+  const long long tiles = (L.Ttot + per - 1) / per;
   int best = 1;
-  long long cost = -1;
-  for (int s = 1; s <= kMaxSplit && (s == 1 || s < 2 * tiles); s *= 2) {
-    const long long waves = (pairs * s + resident - 1) / resident;
-    const long long c = waves * ((tiles + s - 1) / s);
-    if (cost < 0 || c < cost) {
+  double cost = 0.0;
+  for (int s = 1; s <= kMaxSplit && (s == 1 || s <= tiles); ++s) {
+    double c;
+    if (L.T > 0) {
+      const double share = std::ceil(pairs * s / kSms);
+      c = share * static_cast<double>((tiles + s - 1) / s + 1) *
+          (share == 1.0 ? 1.5 : s > 12 ? 1.3 : 1.0);
+    } else {
+      c = pairs * static_cast<double>(tiles + s) / kSms + 4.0 * static_cast<double>(tiles) / s;
+    }
+    c *= 1.0 + 0.04 * s;
+    if (s == 1 || c < cost) {
       cost = c;
       best = s;
     }
   }
   return best;
 }
-constexpr int kFwdResident = 3 * 148, kBwdResident = 2 * 148;
 
 // Fills the common arguments and launches `kern` on clusters of `split` CTAs.
 template <typename... P, typename... A>
-cudaError_t launch_split(void (*kern)(P...), size_t smem, long long blocks, int split,
+cudaError_t launch_split(void (*kern)(P...), int threads, size_t smem, long long blocks, int split,
                          cudaStream_t s, A... args) {
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
@@ -753,7 +774,7 @@ cudaError_t launch_split(void (*kern)(P...), size_t smem, long long blocks, int 
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -768,8 +789,8 @@ cudaError_t launch_split(void (*kern)(P...), size_t smem, long long blocks, int 
 
 }  // namespace
 
-long long glr_bwd_partial_rows(int nseq, long long Ttot, int D) {
-  return static_cast<long long>(nseq) * split_of(nseq, Ttot, D, kBwdResident);
+long long glr_bwd_partial_rows(const SeqLayout& L, int D) {
+  return static_cast<long long>(L.nseq) * split_of(L, D);
 }
 
 cudaError_t launch_glr_fwd(const void* x, const void* r, const void* i, DType in_t,
@@ -777,7 +798,7 @@ cudaError_t launch_glr_fwd(const void* x, const void* r, const void* i, DType in
                            float* state_out, void* h, DType h_t, float* chunk_states, int D,
                            unsigned* err, cudaStream_t s) {
   Args p{x, r, i, lam, c, L, D, (D + kChan - 1) / kChan,
-         split_of(L.nseq, L.Ttot, D, kFwdResident), err};
+         split_of(L, D), err};
   const long long blocks = static_cast<long long>(p.groups) * L.nseq * p.split;
   return by_type(in_t, [&](auto ti) {
     return by_type(h_t, [&](auto th) {
@@ -785,8 +806,8 @@ cudaError_t launch_glr_fwd(const void* x, const void* r, const void* i, DType in
         using Ti = decltype(ti);
         using Th = decltype(th);
         constexpr int M = decltype(mode)::value;
-        const size_t smem = exchange_bytes(p.split) + 2 * 3 * kWarps * run_bytes<Ti, M>();
-        return launch_split(glr_fwd_kernel<Ti, Th, M>, smem, blocks, p.split, s, p, state_in,
+        const size_t smem = exchange_bytes(p.split) + 2 * 3 * kFwdWarps * run_bytes<Ti, M, kFwdRun>();
+        return launch_split(glr_fwd_kernel<Ti, Th, M>, kFwdWarps * 32, smem, blocks, p.split, s, p, state_in,
                             state_out, static_cast<Th*>(h), chunk_states);
       });
     });
@@ -800,7 +821,7 @@ cudaError_t launch_glr_bwd(const void* x, const void* r, const void* i, DType in
                            float* d_lam, float* d_state_in, float* partial, int D, unsigned* err,
                            cudaStream_t s) {
   Args p{x, r, i, lam, c, L, D, (D + kChan - 1) / kChan,
-         split_of(L.nseq, L.Ttot, D, kBwdResident), err};
+         split_of(L, D), err};
   const long long blocks = static_cast<long long>(p.groups) * L.nseq * p.split;
   const cudaError_t e = by_type(in_t, [&](auto ti) {
     return by_type(dh_t, [&](auto tu) {
@@ -811,9 +832,9 @@ cudaError_t launch_glr_bwd(const void* x, const void* r, const void* i, DType in
           using Tg = decltype(tg);
           constexpr int M = decltype(mode)::value;
           const size_t smem =
-              exchange_bytes(p.split) + 2 * kWarps * 32 * sizeof(F2) +
-              2 * kWarps * (3 * run_bytes<Ti, M>() + run_bytes<Tu, M>());
-          return launch_split(glr_bwd_kernel<Ti, Tu, Tg, M>, smem, blocks, p.split, s, p,
+              exchange_bytes(p.split) + 2 * kBwdWarps * 32 * sizeof(F2) +
+              2 * kBwdWarps * (3 * run_bytes<Ti, M, kBwdRun>() + run_bytes<Tu, M, kBwdRun>());
+          return launch_split(glr_bwd_kernel<Ti, Tu, Tg, M>, kBwdWarps * 32, smem, blocks, p.split, s, p,
                               chunk_states, static_cast<const Tu*>(d_h), d_state_out,
                               static_cast<Tg*>(dx), static_cast<Tg*>(dr), static_cast<Tg*>(di),
                               d_state_in, partial);

@@ -120,7 +120,7 @@ cudaError_t launch_glr_fwd(const void* x, const void* r, const void* i, DType in
                            const float* lam, float c, const SeqLayout& L, const float* state_in,
                            float* state_out, void* h, DType h_t, float* chunk_states, int D,
                            unsigned* err, cudaStream_t s);
-long long glr_bwd_partial_rows(int nseq, long long Ttot, int D);
+long long glr_bwd_partial_rows(const SeqLayout& L, int D);
 cudaError_t launch_glr_bwd(const void* x, const void* r, const void* i, DType in_t,
                            const float* lam, float c, const SeqLayout& L,
                            const float* chunk_states, const void* d_h, DType dh_t,
