@@ -18,56 +18,61 @@ using namespace norm;
 
 // ---- forward -------------------------------------------------------------------
 
+// Vectors of four channels: with eight (bf16) the float32 weights of a thread are 32 bytes apart
+// from its neighbour's, twice the cache lines per access.
+constexpr int kFwdVec = 4;
+
 template <typename Tx, typename Ty, int TPR, int NV>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
 ln_fwd_kernel(const Tx* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b,
               float eps, float invD, Ty* __restrict__ y, float* __restrict__ mean,
               float* __restrict__ rstd, int ntok, int D) {
+  constexpr int VEC = kFwdVec;
   constexpr int kRows = TPR < 128 ? 128 / TPR : 1;        // rows of a block
   __shared__ float part[2 * (TPR / 32)];
   const int t = threadIdx.x % TPR;
   const long long row = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / TPR;
   if (TPR <= 32 && row >= ntok) return;                   // whole warps
   const size_t base = static_cast<size_t>(row) * D;
-  Raw8<Tx> raw[NV];
+  Raw<Tx, VEC> raw[NV];
   float s[1] = {0.f};
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int c = (k * TPR + t) * 8;
-    if (c < D) raw[k] = load8(x + base + c);
+    const int c = (k * TPR + t) * VEC;
+    if (c < D) raw[k] = load<VEC>(x + base + c);
   }
 #pragma unroll
   for (int k = 0; k < NV; ++k)
-    if ((k * TPR + t) * 8 < D) {
-      float v[8];
+    if ((k * TPR + t) * VEC < D) {
+      float v[VEC];
       unpack(raw[k], v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] += v[e];
+      for (int e = 0; e < VEC; ++e) s[0] += v[e];
     }
   row_sum<TPR>(s, part, 0);
   const float mu = s[0] * invD;
   s[0] = 0.f;
 #pragma unroll
   for (int k = 0; k < NV; ++k)
-    if ((k * TPR + t) * 8 < D) {
-      float v[8];
+    if ((k * TPR + t) * VEC < D) {
+      float v[VEC];
       unpack(raw[k], v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] = fmaf(v[e] - mu, v[e] - mu, s[0]);
+      for (int e = 0; e < VEC; ++e) s[0] = fmaf(v[e] - mu, v[e] - mu, s[0]);
     }
   row_sum<TPR>(s, part, 1);
   const float rs = inv_std(s[0] * invD, eps);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int c = (k * TPR + t) * 8;
+    const int c = (k * TPR + t) * VEC;
     if (c < D) {
-      float v[8], wv[8], bv[8];
+      float v[VEC], wv[VEC], bv[VEC];
       unpack(raw[k], v);
-      weights8(w, c, 1.f, wv);
-      weights8(b, c, 0.f, bv);
+      weights(w, c, 1.f, wv);
+      weights(b, c, 0.f, bv);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = fmaf((v[e] - mu) * rs, wv[e], bv[e]);
-      store8(y + base + c, v);
+      for (int e = 0; e < VEC; ++e) v[e] = fmaf((v[e] - mu) * rs, wv[e], bv[e]);
+      store(y + base + c, v);
     }
   }
   if (t == 0) {
@@ -116,20 +121,16 @@ ln_fwd_any_kernel(Any x, const float* __restrict__ w, const float* __restrict__ 
 
 // ---- gradients -------------------------------------------------------------------
 
-// A block holds several rows where they are short; blocks of 64 registers per thread fill half
-// an SM's threads.
-#ifndef BNV
-#define BNV 2
-#endif
+// A block holds several rows where they are short.
 constexpr int bwd_threads(int TPR) { return TPR < 256 ? 256 : TPR; }
-constexpr int bwd_blocks_per_sm(int TPR, int NV) { return TPR > 256 ? 1 : NV > 2 ? 1 : NV == 2 ? 2 : 4; }
-
-// 16-byte units of a thread and stage, and the stages (rows on their way, and one in use).
-template <typename Tx, typename Tu> constexpr int bwd_units(int NV) {
-  return NV * (Raw8<Tx>::kU + Raw8<Tu>::kU);
+constexpr int bwd_blocks_per_sm(int TPR) { return TPR > 256 ? 1 : 2; }      // 128 registers
+// Bytes of a stage (a row of x and of d_y per row group, and its statistics), and the stages (rows
+// on their way, and one in use).  CH: channels of a thread.
+template <typename Tx, typename Tu> constexpr int bwd_stage_bytes(int TPR, int CH) {
+  return bwd_threads(TPR) * CH * static_cast<int>(sizeof(Tx) + sizeof(Tu)) + bwd_threads(TPR) / 32 * 8;
 }
-template <typename Tx, typename Tu> constexpr int bwd_stages(int TPR, int NV) {
-  return stages(bwd_units<Tx, Tu>(NV) * bwd_threads(TPR) * 16, bwd_blocks_per_sm(TPR, NV));
+template <typename Tx, typename Tu> constexpr int bwd_stages(int TPR, int CH) {
+  return stages(bwd_stage_bytes<Tx, Tu>(TPR, CH), bwd_blocks_per_sm(TPR));
 }
 
 // Adds the sums of the block's row groups (`acc`, groups x D) in order.
@@ -146,33 +147,43 @@ __device__ __forceinline__ void write_partial(const float* acc, float* out, int 
   __syncthreads();
 }
 
-template <typename Tx, typename Tu, typename Tg, int TPR, int NV>
-__global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks_per_sm(TPR, NV))
+template <typename Tx, typename Tu, typename Tg, int TPR, int CH>
+__global__ void __launch_bounds__(bwd_threads(TPR), bwd_blocks_per_sm(TPR))
 ln_bwd_kernel(const Tx* __restrict__ x, const Tu* __restrict__ dy, const float* __restrict__ mean,
               const float* __restrict__ rstd, const float* __restrict__ w, Tg* __restrict__ dx,
               float* __restrict__ partial, int ntok, int D) {
+  constexpr int VEC = vec_of<Tx, Tu, Tg>(), NV = CH / VEC;
   constexpr int kThreads = bwd_threads(TPR), kGroups = kThreads / TPR;
-  constexpr int kUx = Raw8<Tx>::kU, kUu = Raw8<Tu>::kU;
-  constexpr int kUnits = bwd_units<Tx, Tu>(NV), kStages = bwd_stages<Tx, Tu>(TPR, NV);
+  constexpr int kStages = bwd_stages<Tx, Tu>(TPR, CH), kStage = bwd_stage_bytes<Tx, Tu>(TPR, CH);
+  constexpr int kDy = kThreads * CH * static_cast<int>(sizeof(Tx));           // offsets in a stage
+  constexpr int kStats = kDy + kThreads * CH * static_cast<int>(sizeof(Tu));
+  constexpr bool kHold = CH <= 16;        // weights stay in registers
   extern __shared__ __align__(16) char smem[];
   __shared__ float parts[kGroups][2 * 2 * (TPR > 32 ? TPR / 32 : 1)];
-  const int group = threadIdx.x / TPR;
+  const int group = threadIdx.x / TPR, lane = threadIdx.x & 31;
   float* part = parts[group];
-  uint4* ring = reinterpret_cast<uint4*>(smem) + threadIdx.x;
+  char* xs = smem + threadIdx.x * Raw<Tx, VEC>::kBytes;
+  char* us = smem + kDy + threadIdx.x * Raw<Tu, VEC>::kBytes;
+  char* stats = smem + kStats + (threadIdx.x >> 5) * 8;    // of the warp: mean, rstd
   const int t = threadIdx.x % TPR;
   const int step = gridDim.x * kGroups;
   int row = blockIdx.x * kGroups + group;
   const auto fetch = [&](int r, int stage) {
     if (r < ntok) {
-      uint4* s = ring + stage * (kUnits * kThreads);
       const size_t base = static_cast<size_t>(r) * D;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int c = (k * TPR + t) * 8;
+        const int c = (k * TPR + t) * VEC;
         if (c < D) {
-          copy8(s + k * kUx * kThreads, kThreads, x + base + c);
-          copy8(s + (NV * kUx + k * kUu) * kThreads, kThreads, dy + base + c);
+          copy<VEC, kThreads>(xs + stage * kStage, k, x + base + c);
+          copy<VEC, kThreads>(us + stage * kStage, k, dy + base + c);
         }
+      }
+      // one lane copies for its warp; a load here would hold up every row (0.100 ms instead of
+      // 0.067 ms at 16384 x 4096 bf16)
+      if (lane == 0) {
+        copy_bytes<4>(stats + stage * kStage, mean + r);
+        copy_bytes<4>(stats + stage * kStage + 4, rstd + r);
       }
     }
     copies_commit();
@@ -184,69 +195,66 @@ ln_bwd_kernel(const Tx* __restrict__ x, const Tu* __restrict__ dy, const float* 
   };
 #pragma unroll
   for (int k = 0; k < kStages - 1; ++k) fetch(ahead(k), k);
-  float wv[NV][8], dw[NV][8], db[NV][8];
+  float wv[kHold ? NV : 1][VEC], dw[NV][VEC], db[NV][VEC];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int c = (k * TPR + t) * 8;
-    if (c < D) weights8(w, c, 1.f, wv[k]);
+    const int c = (k * TPR + t) * VEC;
+    if (kHold && c < D) weights(w, c, 1.f, wv[k]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (c >= D) wv[k][e] = 0.f;
-      dw[k][e] = db[k][e] = 0.f;
-    }
+    for (int e = 0; e < VEC; ++e) dw[k][e] = db[k][e] = 0.f;
   }
-  float mu = row < ntok ? mean[row] : 0.f, rs = row < ntok ? rstd[row] : 0.f;
   const float invD = 1.0f / D;
   int use = 0, fill = kStages - 1;
   for (int it = 0; row < ntok; ++it) {
     fetch(ahead(kStages - 1), fill);
-    const int next = ahead(1);
-    const float mu_next = next < ntok ? mean[next] : 0.f, rs_next = next < ntok ? rstd[next] : 0.f;
     copies_wait<kStages - 1>();
-    const uint4* s = ring + use * (kUnits * kThreads);
-    Raw8<Tx> xr[NV];
-    Raw8<Tu> ur[NV];
+    __syncwarp();
+    const float2 st = *reinterpret_cast<const float2*>(stats + use * kStage);
+    const float mu = st.x, rs = st.y;
+    const char* xr = xs + use * kStage;
+    const char* ur = us + use * kStage;
     float sum[2] = {0.f, 0.f};            // of n, and of n (x - mean)
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if ((k * TPR + t) * 8 < D) {
-        xr[k] = read8<Tx>(s + k * kUx * kThreads, kThreads);
-        ur[k] = read8<Tu>(s + (NV * kUx + k * kUu) * kThreads, kThreads);
-        float xv[8], uv[8];
-        unpack(xr[k], xv);
-        unpack(ur[k], uv);
+    for (int k = 0; k < NV; ++k) {
+      const int c = (k * TPR + t) * VEC;
+      if (c < D) {
+        float xv[VEC], uv[VEC], wl[VEC];
+        unpack(staged<Tx, VEC, kThreads>(xr, k), xv);
+        unpack(staged<Tu, VEC, kThreads>(ur, k), uv);
+        if (!kHold) weights(w, c, 1.f, wl);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float n = uv[e] * wv[k][e];
+        for (int e = 0; e < VEC; ++e) {
+          const float n = uv[e] * (kHold ? wv[kHold ? k : 0][e] : wl[e]);
           sum[0] += n;
           sum[1] = fmaf(n, xv[e] - mu, sum[1]);
         }
       }
+    }
     row_sum<TPR>(sum, part, it, group);
     const float m1 = -rs * sum[0] * invD, m2 = -rs * rs * sum[1] * invD;
     const size_t base = static_cast<size_t>(row) * D;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (k * TPR + t) * 8;
+      const int c = (k * TPR + t) * VEC;
       if (c < D) {
-        float xv[8], uv[8], g[8];
-        unpack(xr[k], xv);
-        unpack(ur[k], uv);
+        float xv[VEC], uv[VEC], wl[VEC], g[VEC];
+        unpack(staged<Tx, VEC, kThreads>(xr, k), xv);
+        unpack(staged<Tu, VEC, kThreads>(ur, k), uv);
+        if (!kHold) weights(w, c, 1.f, wl);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < VEC; ++e) {
           const float xh = (xv[e] - mu) * rs;
           dw[k][e] = fmaf(uv[e], xh, dw[k][e]);
           db[k][e] += uv[e];
-          g[e] = fmaf(xh, m2, fmaf(uv[e] * wv[k][e], rs, m1));
+          g[e] = fmaf(xh, m2, fmaf(uv[e] * (kHold ? wv[kHold ? k : 0][e] : wl[e]), rs, m1));
         }
-        store8(dx + base + c, g);
+        store(dx + base + c, g);
       }
     }
+    __syncwarp();                         // the warp's statistics are read before their refill
     fill = use;
     use = use + 1 == kStages ? 0 : use + 1;
-    row = next;
-    mu = mu_next;
-    rs = rs_next;
+    row = ahead(1);
   }
   if (!partial) return;
   copies_wait<0>();
@@ -254,10 +262,10 @@ ln_bwd_kernel(const Tx* __restrict__ x, const Tu* __restrict__ dy, const float* 
   if constexpr (kGroups == 1) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (k * TPR + t) * 8;
+      const int c = (k * TPR + t) * VEC;
       if (c < D) {
-        store8(mine + c, dw[k]);
-        store8(mine + static_cast<size_t>(gridDim.x) * D + c, db[k]);
+        store(mine + c, dw[k]);
+        store(mine + static_cast<size_t>(gridDim.x) * D + c, db[k]);
       }
     }
   } else {
@@ -266,11 +274,11 @@ ln_bwd_kernel(const Tx* __restrict__ x, const Tu* __restrict__ dy, const float* 
     __syncthreads();                      // every group has read its rows from the ring
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if ((k * TPR + t) * 8 < D) store8(own + (k * TPR + t) * 8, dw[k]);
+      if ((k * TPR + t) * VEC < D) store(own + (k * TPR + t) * VEC, dw[k]);
     write_partial<TPR>(acc, mine, D);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if ((k * TPR + t) * 8 < D) store8(own + (k * TPR + t) * 8, db[k]);
+      if ((k * TPR + t) * VEC < D) store(own + (k * TPR + t) * VEC, db[k]);
     write_partial<TPR>(acc, mine + static_cast<size_t>(gridDim.x) * D, D);
   }
 }
@@ -348,92 +356,79 @@ ln_bwd_any_kernel(Any x, Any dy, const float* __restrict__ mean, const float* __
 
 // ---- which variant -----------------------------------------------------------------
 
-// Threads and values per thread of a row; D <= tpr * nv * vec.
+// Threads of a row and channels of each; D <= tpr * ch.
 struct Shape {
-  int vec, tpr, nv;
+  bool vec;
+  int tpr, ch;
 };
 
-// Forward: a warp per row up to 1024 channels, otherwise a block with up to four vectors per
-// thread; few rows (at most two per SM) get a thread for every vector or two instead, since the
-// row's own latency counts then.
+// Forward: a warp per row up to 1024 channels, otherwise a block with 32 channels per thread; few
+// rows (at most two per SM) get more threads instead, since the row's own latency counts then.
 Shape fwd_shape(int ntok, int D) {
+  const bool few = ntok <= 2 * kSms;
   if (D % 8 == 0) {
-    const int n = D / 8;
-    const bool few = ntok <= 2 * kSms;
-    if (n <= 32) return {8, 32, 1};
-    if (n <= 64) return {8, 32, 2};
-    if (n <= 128 && !few) return {8, 32, 4};
-    if (n <= 256) return {8, 128, 2};
-#ifdef LNF
-    if (n <= 512) return few ? Shape{8, 512, 1} : Shape{8, LNF, 512/LNF};
-#endif
-    if (n <= 512) return few ? Shape{8, 512, 1} : Shape{8, 128, 4};
-    if (n <= 1024) return few ? Shape{8, 512, 2} : Shape{8, 256, 4};
-    return {8, 512, 4};
+    if (D <= 256) return {true, 32, 8};
+    if (D <= 512) return {true, 32, 16};
+    if (few && D <= 4096) return D <= 1024 ? Shape{true, 128, 8} : Shape{true, 512, 8};
+    if (D <= 1024) return {true, 32, 32};
+    if (D <= 4096) return {true, 128, 32};
+    if (D <= 8192) return {true, 256, 32};
+    return {true, 512, 32};
   }
-  if (D <= 256) return {1, 32, 8};
-  if (D <= 1024) return {1, 128, 8};
-  if (D <= 4096) return {1, 256, 16};
-  return {1, 512, 32};
+  if (D <= 256) return {false, 32, 8};
+  if (D <= 1024) return {false, 128, 8};
+  if (D <= 4096) return {false, 256, 16};
+  return {false, 512, 32};
 }
-// Gradients: one vector per thread where a block can be that large (three values stay in
-// registers for each channel).
+// Gradients: 16 channels per thread, of which three values each stay in registers; 32 where a
+// block cannot be larger, and their weights are read again for every row.
 Shape bwd_shape(int D) {
   if (D % 8 == 0) {
-    const int n = D / 8;
-    int tpr = 32, nv = BNV;
-    while (tpr * nv < n && tpr < 512) tpr *= 2;
-    if (tpr * nv < n) nv = n <= 1024 ? 2 : 4;
-    return {8, tpr, nv};
+    int tpr = 32;
+    while (tpr < 512 && tpr * 16 < D) tpr *= 2;
+    return {true, tpr, tpr * 16 < D ? 32 : 16};
   }
-  if (D <= 256) return {1, 32, 8};
-  if (D <= 1024) return {1, 128, 8};
-  if (D <= 4096) return {1, 256, 16};
-  return {1, 512, 32};
+  if (D <= 256) return {false, 32, 8};
+  if (D <= 1024) return {false, 128, 8};
+  if (D <= 4096) return {false, 256, 16};
+  return {false, 512, 32};
 }
 
 template <int T, int N> struct Pick {
-  static constexpr int tpr = T, nv = N;
+  static constexpr int tpr = T, ch = N;
 };
 template <typename F>
 cudaError_t with_shape(const Shape& s, F&& f) {
-  switch (s.tpr * 64 + s.nv) {
-    case 32 * 64 + 1: return f(Pick<32, 1>{});
-    case 32 * 64 + 2: return f(Pick<32, 2>{});
-    case 32 * 64 + 4: return f(Pick<32, 4>{});
+  switch (s.tpr * 64 + s.ch) {
     case 32 * 64 + 8: return f(Pick<32, 8>{});
-    case 64 * 64 + 1: return f(Pick<64, 1>{});
-    case 64 * 64 + 2: return f(Pick<64, 2>{});
-    case 64 * 64 + 4: return f(Pick<64, 4>{});
-    case 128 * 64 + 1: return f(Pick<128, 1>{});
-    case 128 * 64 + 2: return f(Pick<128, 2>{});
-    case 128 * 64 + 4: return f(Pick<128, 4>{});
+    case 32 * 64 + 16: return f(Pick<32, 16>{});
+    case 32 * 64 + 32: return f(Pick<32, 32>{});
+    case 64 * 64 + 16: return f(Pick<64, 16>{});
     case 128 * 64 + 8: return f(Pick<128, 8>{});
-    case 256 * 64 + 1: return f(Pick<256, 1>{});
-    case 256 * 64 + 2: return f(Pick<256, 2>{});
-    case 256 * 64 + 4: return f(Pick<256, 4>{});
+    case 128 * 64 + 16: return f(Pick<128, 16>{});
+    case 128 * 64 + 32: return f(Pick<128, 32>{});
     case 256 * 64 + 16: return f(Pick<256, 16>{});
-    case 512 * 64 + 1: return f(Pick<512, 1>{});
-    case 512 * 64 + 2: return f(Pick<512, 2>{});
-    case 512 * 64 + 4: return f(Pick<512, 4>{});
+    case 256 * 64 + 32: return f(Pick<256, 32>{});
+    case 512 * 64 + 8: return f(Pick<512, 8>{});
+    case 512 * 64 + 16: return f(Pick<512, 16>{});
     case 512 * 64 + 32: return f(Pick<512, 32>{});
-    case 1024 * 64 + 1: return f(Pick<1024, 1>{});
   }
   return cudaErrorInvalidConfiguration;
 }
 // Compiles only what a shape table can name.
-constexpr bool fwd_vec(int tpr, int nv) {
-  return (tpr == 32 && nv <= 4) || (tpr == 128 && nv >= 2 && nv <= 4) || (tpr == 256 && (nv == 2 || nv == 4)) ||
-         (tpr == 512 && nv <= 4);
+constexpr bool fwd_vec(int tpr, int ch) {
+  return tpr == 32 || (tpr == 128 && ch != 16) || (tpr == 256 && ch == 32) ||
+         (tpr == 512 && ch != 16);
 }
-constexpr bool bwd_vec(int tpr, int nv) { return tpr <= 512 && (nv == BNV || (tpr == 512 && nv >= 2 && nv <= 4)); }
-constexpr bool any_width(int tpr, int nv) {
-  return (tpr <= 128 && nv == 8) || (tpr == 256 && nv == 16) || (tpr == 512 && nv == 32);
+constexpr bool bwd_vec(int tpr, int ch) { return ch == 16 || (tpr == 512 && ch == 32); }
+constexpr bool any_width(int tpr, int ch) {
+  return (tpr == 32 && ch == 8) || (tpr == 128 && ch == 8) || (tpr == 256 && ch == 16) ||
+         (tpr == 512 && ch == 32);
 }
 
 int bwd_blocks(const Shape& s, int ntok) {
   const int groups = bwd_threads(s.tpr) / s.tpr;
-  const int per_sm = s.vec == 1 ? (s.tpr > 256 ? 1 : 4) : bwd_blocks_per_sm(s.tpr, s.nv);
+  const int per_sm = s.vec ? bwd_blocks_per_sm(s.tpr) : s.tpr > 256 ? 1 : 4;
   const int need = (ntok + groups - 1) / groups;
   return need < kSms * per_sm ? need : kSms * per_sm;
 }
@@ -449,8 +444,8 @@ cudaError_t launch_layer_norm_fwd(const void* x, DType x_t, const float* w, cons
   const unsigned blocks = static_cast<unsigned>((ntok + static_cast<long long>(rows) - 1) / rows);
   const int threads = sh.tpr < 128 ? 128 : sh.tpr;
   return with_shape(sh, [&](auto p) {
-    constexpr int T = decltype(p)::tpr, N = decltype(p)::nv;
-    if (sh.vec == 1) {
+    constexpr int T = decltype(p)::tpr, N = decltype(p)::ch;
+    if (!sh.vec) {
       if constexpr (any_width(T, N)) {
         ln_fwd_any_kernel<T, N><<<blocks, threads, 0, s>>>(Any{x, x_t == DType::F32}, w, b, eps,
                                                           invD, AnyOut{y, y_t == DType::F32}, mean, rstd,
@@ -462,7 +457,7 @@ cudaError_t launch_layer_norm_fwd(const void* x, DType x_t, const float* w, cons
         return by_type(y_t, [&](auto ty) {
           using Tx = decltype(tx);
           using Ty = decltype(ty);
-          ln_fwd_kernel<Tx, Ty, T, N><<<blocks, threads, 0, s>>>(
+          ln_fwd_kernel<Tx, Ty, T, N / kFwdVec><<<blocks, threads, 0, s>>>(
               static_cast<const Tx*>(x), w, b, eps, invD, static_cast<Ty*>(y), mean, rstd, ntok, D);
           return cudaGetLastError();
         });
@@ -484,10 +479,10 @@ cudaError_t launch_layer_norm_bwd(const void* x, DType x_t, const void* dy, DTyp
   cudaError_t e = cudaSuccess;
   if (blocks > 0)
     e = with_shape(sh, [&](auto p) {
-      constexpr int T = decltype(p)::tpr, N = decltype(p)::nv;
+      constexpr int T = decltype(p)::tpr, N = decltype(p)::ch;
       constexpr int kThreads = bwd_threads(T);
       const size_t sums = kThreads / T > 1 ? static_cast<size_t>(kThreads / T) * D * sizeof(float) : 0;
-      if (sh.vec == 1) {
+      if (!sh.vec) {
         if constexpr (any_width(T, N)) {
           const cudaError_t a = allow_smem(ln_bwd_any_kernel<T, N>, sums);
           if (a != cudaSuccess) return a;
@@ -503,8 +498,8 @@ cudaError_t launch_layer_norm_bwd(const void* x, DType x_t, const void* dy, DTyp
               using Tx = decltype(tx);
               using Tu = decltype(tu);
               using Tg = decltype(tg);
-              const size_t ring = static_cast<size_t>(bwd_stages<Tx, Tu>(T, N)) *
-                                  bwd_units<Tx, Tu>(N) * kThreads * sizeof(uint4);
+              const size_t ring =
+                  static_cast<size_t>(bwd_stages<Tx, Tu>(T, N)) * bwd_stage_bytes<Tx, Tu>(T, N);
               const size_t smem = ring > sums ? ring : sums;
               const cudaError_t a = allow_smem(ln_bwd_kernel<Tx, Tu, Tg, T, N>, smem);
               if (a != cudaSuccess) return a;

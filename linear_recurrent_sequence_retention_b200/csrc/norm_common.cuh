@@ -1,11 +1,14 @@
 // Shared by layer norm, its gradients and the gradients of the GroupNorm + gate:
-// how a row is spread over threads, eight-element vectors, sums over a row's
+// how a row is spread over threads, vectors, sums over a row's
 // threads, per-thread copies into shared memory ahead of use, and the sum of the
 // partial weight gradients.
 //
-// A row of D channels belongs to TPR threads; with VEC = 8 thread t of them holds
-// the vectors t, t + TPR, ... (NV of them) of eight channels, with VEC = 1 (rows
-// that do not divide into such vectors) the channels t, t + TPR, ...
+// A row of D channels belongs to TPR threads; thread t of them holds the vectors t, t + TPR,
+// ... (NV of them) of VEC channels.  A vector is at most 16 bytes of any tensor, so that the
+// threads of a warp touch whole sectors with every access: VEC = 8 where all tensors are bf16,
+// 4 where one is float32 (with 32-byte vectors every sector is fetched twice: the gradients of a
+// float32 layer norm at 4096 x 4096 took 0.054 ms that way).  VEC = 1 serves rows that do not
+// divide by eight.
 #pragma once
 
 #include "launch.h"
@@ -40,56 +43,74 @@ struct AnyOut {
   }
 };
 
-// Eight consecutive elements as they are stored.
-template <typename T> struct Raw8 {
-  static constexpr int kU = static_cast<int>(sizeof(T)) / 2;     // 16-byte units
-  uint4 u[kU];
+// VEC consecutive elements as they are stored: 8 or 16 bytes.
+template <typename T, int VEC> struct Raw {
+  static constexpr int kBytes = VEC * static_cast<int>(sizeof(T));
+  static constexpr int kWords = kBytes / 4;
+  static_assert(kBytes == 8 || kBytes == 16, "one access");
+  uint32_t w[kWords];
 };
-template <typename T>
-__device__ __forceinline__ Raw8<T> load8(const T* p) {
-  Raw8<T> r;
-#pragma unroll
-  for (int k = 0; k < Raw8<T>::kU; ++k) r.u[k] = __ldg(reinterpret_cast<const uint4*>(p) + k);
+template <int WORDS>
+__device__ __forceinline__ void load_words(uint32_t (&w)[WORDS], const void* p) {
+  if constexpr (WORDS == 4) {
+    const uint4 v = *static_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else {
+    const uint2 v = *static_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  }
+}
+template <int VEC, typename T>
+__device__ __forceinline__ Raw<T, VEC> load(const T* p) {
+  Raw<T, VEC> r;
+  load_words(r.w, p);
   return r;
 }
-__device__ __forceinline__ void unpack(const Raw8<__nv_bfloat16>& r, float (&v)[8]) {
-  const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
+template <int VEC>
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, VEC>& r, float (&v)[VEC]) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    v[2 * k] = __uint_as_float(w[k] << 16);
-    v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+  for (int k = 0; k < VEC / 2; ++k) {
+    v[2 * k] = __uint_as_float(r.w[k] << 16);
+    v[2 * k + 1] = __uint_as_float(r.w[k] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void unpack(const Raw8<float>& r, float (&v)[8]) {
+template <int VEC>
+__device__ __forceinline__ void unpack(const Raw<float, VEC>& r, float (&v)[VEC]) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    v[4 * k] = __uint_as_float(r.u[k].x);
-    v[4 * k + 1] = __uint_as_float(r.u[k].y);
-    v[4 * k + 2] = __uint_as_float(r.u[k].z);
-    v[4 * k + 3] = __uint_as_float(r.u[k].w);
-  }
+  for (int k = 0; k < VEC; ++k) v[k] = __uint_as_float(r.w[k]);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  uint32_t w[4];
+template <int VEC>
+__device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[VEC]) {
+  uint32_t w[VEC / 2];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < VEC / 2; ++k) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
     w[k] = *reinterpret_cast<const uint32_t*>(&b);
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  if constexpr (VEC == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  else
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-// Eight weights; `none` where there are none.
-__device__ __forceinline__ void weights8(const float* w, int c, float none, float (&v)[8]) {
-  if (w) {
-    unpack(load8(w + c), v);
-  } else {
+template <int VEC>
+__device__ __forceinline__ void store(float* p, const float (&v)[VEC]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = none;
+  for (int k = 0; k < VEC; k += 4)
+    *reinterpret_cast<float4*>(p + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+}
+// VEC weights; `none` where there are none.
+template <int VEC>
+__device__ __forceinline__ void weights(const float* w, int c, float none, float (&v)[VEC]) {
+#pragma unroll
+  for (int k = 0; k < VEC; k += 4) {
+    const float4 f = w ? __ldg(reinterpret_cast<const float4*>(w + c + k))
+                       : make_float4(none, none, none, none);
+    v[k] = f.x, v[k + 1] = f.y, v[k + 2] = f.z, v[k + 3] = f.w;
   }
+}
+// 8 where every tensor is bf16, else 4.
+template <typename... T> constexpr int vec_of() {
+  return ((sizeof(T) == 2) && ...) ? 8 : 4;
 }
 
 // 1 / sqrt(var + eps), to two units of the last place: a row's one reciprocal root costs every
@@ -127,34 +148,36 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* part, int turn, in
 // ---- copies ahead of use ---------------------------------------------------------
 
 // Every thread copies the vectors that it will read itself, so the only wait is for its own
-// copies.  Unit n of thread t lies at [n][t]: no bank conflicts.
-__device__ __forceinline__ void copy16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-               "l"(src)
-               : "memory");
+// copies.  Vector n of thread t lies at [n][t]: no bank conflicts.
+template <int BYTES>
+__device__ __forceinline__ void copy_bytes(void* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES)
+                 : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// Stages of `bytes` each that fit where `blocks` blocks share an SM: at most four.
+// Stages of `bytes` each that fit where `blocks` blocks share an SM: at most four (more
+// made no difference).
 constexpr int stages(int bytes, int blocks) {
-  const int fit = (220 * 1024 / blocks) / bytes;
+  const int fit = (216 * 1024 / blocks) / bytes;
   return fit > 4 ? 4 : fit < 1 ? 1 : fit;
 }
-template <typename T>
-__device__ __forceinline__ void copy8(uint4* slot, int threads, const T* src) {
-#pragma unroll
-  for (int k = 0; k < Raw8<T>::kU; ++k)
-    copy16(slot + k * threads, reinterpret_cast<const uint4*>(src) + k);
+// `slot`: the thread's place in the first vector of a tensor's part of a stage.
+template <int VEC, int THREADS, typename T>
+__device__ __forceinline__ void copy(char* slot, int n, const T* src) {
+  copy_bytes<Raw<T, VEC>::kBytes>(slot + n * (THREADS * Raw<T, VEC>::kBytes), src);
 }
-template <typename T>
-__device__ __forceinline__ Raw8<T> read8(const uint4* slot, int threads) {
-  Raw8<T> r;
-#pragma unroll
-  for (int k = 0; k < Raw8<T>::kU; ++k) r.u[k] = slot[k * threads];
+template <typename T, int VEC, int THREADS>
+__device__ __forceinline__ Raw<T, VEC> staged(const char* slot, int n) {
+  Raw<T, VEC> r;
+  load_words(r.w, slot + n * (THREADS * Raw<T, VEC>::kBytes));
   return r;
 }
 

@@ -16,12 +16,13 @@ using namespace norm;
 constexpr int kThreads = 256;
 // Blocks of an SM: 128 registers per thread.
 constexpr int kBlocksPerSm = 2;
-// 16-byte units of a thread and stage, and the stages (rows on their way, and one in use).
-template <typename To, typename Ti> constexpr int row_units(int NV) {
-  return NV * (Raw8<To>::kU + 2 * Raw8<Ti>::kU);
+// Bytes of a stage (a row of o, g and d_y per group), and the stages (rows on their way, and one
+// in use).  CH: channels of a thread.
+template <typename To, typename Ti> constexpr int stage_bytes(int CH) {
+  return kThreads * CH * static_cast<int>(sizeof(To) + 2 * sizeof(Ti));
 }
-template <typename To, typename Ti> constexpr int row_stages(int NV) {
-  return stages(row_units<To, Ti>(NV) * kThreads * 16, kBlocksPerSm);
+template <typename To, typename Ti> constexpr int stage_count(int CH) {
+  return stages(stage_bytes<To, Ti>(CH), kBlocksPerSm);
 }
 
 // swish(g) = g s and its derivative's factor s (1 + g (1 - s)), s = sigmoid(g)
@@ -29,36 +30,39 @@ __device__ __forceinline__ float sigmoid(float x) {
   return __fdividef(1.0f, 1.0f + __expf(-x));
 }
 
-template <typename To, typename Ti, typename Tg, int TPR, int NV>
+template <typename To, typename Ti, typename Tg, int TPR, int CH>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 ng_bwd_kernel(const To* __restrict__ o, const Ti* __restrict__ g, const Ti* __restrict__ dy,
               const float* __restrict__ w, const float* __restrict__ b, float eps,
               Tg* __restrict__ d_o, Tg* __restrict__ d_g, float* __restrict__ partial, int ntok,
               int H, int dv, int lanes) {
-  constexpr int kUo = Raw8<To>::kU, kUi = Raw8<Ti>::kU;
-  constexpr int kUnits = row_units<To, Ti>(NV), kStages = row_stages<To, Ti>(NV);
+  constexpr int VEC = vec_of<To, Ti, Tg>(), NV = CH / VEC;
+  constexpr int kStages = stage_count<To, Ti>(CH), kStage = stage_bytes<To, Ti>(CH);
+  constexpr int kG = kThreads * CH * static_cast<int>(sizeof(To));      // offsets in a stage
+  constexpr int kDy = kG + kThreads * CH * static_cast<int>(sizeof(Ti));
   constexpr int kW = TPR > 32 ? TPR / 32 : 1;
   extern __shared__ __align__(16) char smem[];
   __shared__ float parts[kThreads / TPR][2 * kW * 4];
-  uint4* ring = reinterpret_cast<uint4*>(smem) + threadIdx.x;
+  char* os = smem + threadIdx.x * Raw<To, VEC>::kBytes;
+  char* gs = smem + kG + threadIdx.x * Raw<Ti, VEC>::kBytes;
+  char* us = smem + kDy + threadIdx.x * Raw<Ti, VEC>::kBytes;
   const int t = threadIdx.x % TPR, local = threadIdx.x / TPR;
   const int group = blockIdx.x * (kThreads / TPR) + local;
   const int head = group % H, first = group / H;      // first: token, and partial row
   const size_t token = static_cast<size_t>(H) * dv, stride = token * lanes;
-  const int col = head * dv + t * 8;                  // of the thread's first vector
+  const int col = head * dv + t * VEC;                  // of the thread's first vector
   bool has[NV];                                       // groups of a warp may differ here
 #pragma unroll
-  for (int k = 0; k < NV; ++k) has[k] = first < lanes && (k * TPR + t) * 8 < dv;
+  for (int k = 0; k < NV; ++k) has[k] = first < lanes && (k * TPR + t) * VEC < dv;
   const auto fetch = [&](bool there, size_t at, int stage) {
     if (there) {
-      uint4* s = ring + stage * (kUnits * kThreads);
 #pragma unroll
       for (int k = 0; k < NV; ++k)
         if (has[k]) {
-          const size_t c = at + k * TPR * 8;
-          copy8(s + k * kUo * kThreads, kThreads, o + c);
-          copy8(s + (NV * kUo + k * kUi) * kThreads, kThreads, g + c);
-          copy8(s + (NV * (kUo + kUi) + k * kUi) * kThreads, kThreads, dy + c);
+          const size_t c = at + k * TPR * VEC;
+          copy<VEC, kThreads>(os + stage * kStage, k, o + c);
+          copy<VEC, kThreads>(gs + stage * kStage, k, g + c);
+          copy<VEC, kThreads>(us + stage * kStage, k, dy + c);
         }
     }
     copies_commit();
@@ -67,11 +71,11 @@ ng_bwd_kernel(const To* __restrict__ o, const Ti* __restrict__ g, const Ti* __re
 #pragma unroll
   for (int k = 0; k < kStages - 1; ++k)
     fetch(first + static_cast<long long>(k) * lanes < ntok, at + k * stride, k);
-  float dw[NV][8], db[NV][8];
+  float dw[NV][VEC], db[NV][VEC];
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[k][e] = db[k][e] = 0.f;
+    for (int e = 0; e < VEC; ++e) dw[k][e] = db[k][e] = 0.f;
   const float invD = 1.0f / dv;
   // all groups of a warp take the same number of turns (the sums are warp-wide shuffles)
   const int turns = (ntok + lanes - 1) / lanes;
@@ -81,27 +85,26 @@ ng_bwd_kernel(const To* __restrict__ o, const Ti* __restrict__ g, const Ti* __re
     const bool ok = n < ntok;
     fetch(n + static_cast<long long>(kStages - 1) * lanes < ntok, at + (kStages - 1) * stride, fill);
     copies_wait<kStages - 1>();
-    const uint4* s = ring + use * (kUnits * kThreads);
-    float ov[NV][8], dt[NV][8], q[NV][8];
+    float ov[NV][VEC], dt[NV][VEC], q[NV][VEC];
     float mean[1] = {0.f}, sum[3] = {0.f, 0.f, 0.f};   // sum: of (o - mu)^2, n and n (o - mu)
 #pragma unroll
     for (int k = 0; k < NV; ++k)
       if (ok && has[k]) {
-        unpack(read8<To>(s + k * kUo * kThreads, kThreads), ov[k]);
+        unpack(staged<To, VEC, kThreads>(os + use * kStage, k), ov[k]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mean[0] += ov[k][e];
+        for (int e = 0; e < VEC; ++e) mean[0] += ov[k][e];
       }
     row_sum<TPR>(mean, parts[local], it, local);
     const float mu = mean[0] * invD;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
       if (ok && has[k]) {
-        float gv[8], uv[8], wv[8];
-        unpack(read8<Ti>(s + (NV * kUo + k * kUi) * kThreads, kThreads), gv);
-        unpack(read8<Ti>(s + (NV * (kUo + kUi) + k * kUi) * kThreads, kThreads), uv);
-        weights8(w, col + k * TPR * 8, 1.f, wv);
+        float gv[VEC], uv[VEC], wv[VEC];
+        unpack(staged<Ti, VEC, kThreads>(gs + use * kStage, k), gv);
+        unpack(staged<Ti, VEC, kThreads>(us + use * kStage, k), uv);
+        weights(w, col + k * TPR * VEC, 1.f, wv);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < VEC; ++e) {
           ov[k][e] -= mu;
           const float sg = sigmoid(gv[e]), us = uv[e] * sg;
           const float d = us * gv[e];                  // d_y swish(g)
@@ -118,19 +121,19 @@ ng_bwd_kernel(const To* __restrict__ o, const Ti* __restrict__ g, const Ti* __re
 #pragma unroll
     for (int k = 0; k < NV; ++k)
       if (ok && has[k]) {
-        float go[8], gg[8], wv[8], bv[8];
-        weights8(w, col + k * TPR * 8, 1.f, wv);
-        weights8(b, col + k * TPR * 8, 0.f, bv);
+        float go[VEC], gg[VEC], wv[VEC], bv[VEC];
+        weights(w, col + k * TPR * VEC, 1.f, wv);
+        weights(b, col + k * TPR * VEC, 0.f, bv);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < VEC; ++e) {
           const float xh = ov[k][e] * rs;
           gg[e] = q[k][e] * fmaf(xh, wv[e], bv[e]);
           go[e] = fmaf(xh, m2, fmaf(dt[k][e] * wv[e], rs, m1));
           dw[k][e] = fmaf(dt[k][e], xh, dw[k][e]);
           db[k][e] += dt[k][e];
         }
-        store8(d_o + at + k * TPR * 8, go);
-        store8(d_g + at + k * TPR * 8, gg);
+        store(d_o + at + k * TPR * VEC, go);
+        store(d_g + at + k * TPR * VEC, gg);
       }
     fill = use;
     use = use + 1 == kStages ? 0 : use + 1;
@@ -142,8 +145,8 @@ ng_bwd_kernel(const To* __restrict__ o, const Ti* __restrict__ g, const Ti* __re
 #pragma unroll
   for (int k = 0; k < NV; ++k)
     if (has[k]) {
-      store8(mine + k * TPR * 8, dw[k]);
-      store8(mine + stride + k * TPR * 8, db[k]);
+      store(mine + k * TPR * VEC, dw[k]);
+      store(mine + stride + k * TPR * VEC, db[k]);
     }
 }
 
@@ -216,15 +219,12 @@ ng_bwd_any_kernel(Any o, Any g, Any dy, const float* __restrict__ w, const float
   }
 }
 
-// Threads of a row, and the vectors of each.
-#ifndef GNV
-#define GNV 2
-#endif
-int row_vectors(int dv) { return dv > 64 * GNV ? GNV : 1; }
+// Channels of a thread, and threads of a row.
+int row_channels(int dv) { return dv > 64 ? 16 : 8; }
 int row_threads(int dv) {
   if (dv % 8 != 0) return 32;
   int t = 8;
-  while (t * 8 * row_vectors(dv) < dv) t *= 2;
+  while (t * row_channels(dv) < dv) t *= 2;
   return t;
 }
 // Token lanes: groups per head that are resident at once.
@@ -268,9 +268,9 @@ cudaError_t launch_norm_gate_bwd(const void* o, DType o_t, const void* g, const 
             using To = decltype(to);
             using Ti = decltype(ti);
             using Tg = decltype(tg);
-            const auto run = [&](auto kern, int nv) {
-              const size_t smem = static_cast<size_t>(row_stages<To, Ti>(nv)) *
-                                  row_units<To, Ti>(nv) * kThreads * sizeof(uint4);
+            const auto run = [&](auto kern, int ch) {
+              const size_t smem =
+                  static_cast<size_t>(stage_count<To, Ti>(ch)) * stage_bytes<To, Ti>(ch);
               const cudaError_t a = allow_smem(kern, smem);
               if (a != cudaSuccess) return a;
               kern<<<blocks, kThreads, smem, s>>>(
@@ -279,15 +279,11 @@ cudaError_t launch_norm_gate_bwd(const void* o, DType o_t, const void* g, const 
                   lanes);
               return cudaGetLastError();
             };
-            if (tpr == 8 && row_vectors(dv) == 1) return run(ng_bwd_kernel<To, Ti, Tg, 8, 1>, 1);
-            if (GNV == 1) {
-            if (tpr == 16) return run(ng_bwd_kernel<To, Ti, Tg, 16, GNV>, GNV);
-            if (tpr == 128) return run(ng_bwd_kernel<To, Ti, Tg, 128, GNV>, GNV);
-            }
-            if (tpr == 16) return run(ng_bwd_kernel<To, Ti, Tg, 16, GNV>, GNV);
-            if (tpr == 32) return run(ng_bwd_kernel<To, Ti, Tg, 32, GNV>, GNV);
-            if (tpr == 64) return run(ng_bwd_kernel<To, Ti, Tg, 64, GNV>, GNV);
-            return run(ng_bwd_kernel<To, Ti, Tg, 8, GNV>, GNV);
+            if (row_channels(dv) == 8) return run(ng_bwd_kernel<To, Ti, Tg, 8, 8>, 8);
+            if (tpr == 8) return run(ng_bwd_kernel<To, Ti, Tg, 8, 16>, 16);
+            if (tpr == 16) return run(ng_bwd_kernel<To, Ti, Tg, 16, 16>, 16);
+            if (tpr == 32) return run(ng_bwd_kernel<To, Ti, Tg, 32, 16>, 16);
+            return run(ng_bwd_kernel<To, Ti, Tg, 64, 16>, 16);
           });
         });
       });
