@@ -81,10 +81,10 @@ ln_fwd_kernel(const Tx* __restrict__ x, const float* __restrict__ w, const float
   }
 }
 
-// Any width, any types: one channel at a time.
-template <int TPR, int NV>
+// Any width: one channel at a time.
+template <typename Tx, int TPR, int NV>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
-ln_fwd_any_kernel(Any x, const float* __restrict__ w, const float* __restrict__ b, float eps,
+ln_fwd_any_kernel(const Tx* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, float eps,
                   float invD, AnyOut y, float* __restrict__ mean, float* __restrict__ rstd, int ntok, int D) {
   constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
   __shared__ float part[2 * (TPR / 32)];
@@ -97,7 +97,7 @@ ln_fwd_any_kernel(Any x, const float* __restrict__ w, const float* __restrict__ 
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = k * TPR + t;
-    v[k] = c < D ? x.ld(base + c) : 0.f;
+    v[k] = c < D ? Io<Tx>::ld(x, base + c) : 0.f;
     s[0] += v[k];
   }
   row_sum<TPR>(s, part, 0);
@@ -257,6 +257,7 @@ ln_bwd_kernel(const Tx* __restrict__ x, const Tu* __restrict__ dy, const float* 
     row = ahead(1);
   }
   if (!partial) return;
+  release_dependents();
   copies_wait<0>();
   float* mine = partial + static_cast<size_t>(blockIdx.x) * D;
   if constexpr (kGroups == 1) {
@@ -283,10 +284,10 @@ ln_bwd_kernel(const Tx* __restrict__ x, const Tu* __restrict__ dy, const float* 
   }
 }
 
-// Any width, any types: one channel at a time.
-template <int TPR, int NV>
+// Any width: one channel at a time.
+template <typename Tx, typename Tu, int TPR, int NV>
 __global__ void __launch_bounds__(bwd_threads(TPR))
-ln_bwd_any_kernel(Any x, Any dy, const float* __restrict__ mean, const float* __restrict__ rstd,
+ln_bwd_any_kernel(const Tx* __restrict__ x, const Tu* __restrict__ dy, const float* __restrict__ mean, const float* __restrict__ rstd,
                   const float* __restrict__ w, AnyOut dx, float* __restrict__ partial, int ntok,
                   int D) {
   constexpr int kThreads = bwd_threads(TPR), kGroups = kThreads / TPR;
@@ -308,8 +309,8 @@ ln_bwd_any_kernel(Any x, Any dy, const float* __restrict__ mean, const float* __
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = k * TPR + t;
-      xv[k] = c < D ? x.ld(base + c) : mu;
-      uv[k] = c < D ? dy.ld(base + c) : 0.f;
+      xv[k] = c < D ? Io<Tx>::ld(x, base + c) : mu;
+      uv[k] = c < D ? Io<Tu>::ld(dy, base + c) : 0.f;
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -330,6 +331,7 @@ ln_bwd_any_kernel(Any x, Any dy, const float* __restrict__ mean, const float* __
     }
   }
   if (!partial) return;
+  release_dependents();
   float* mine = partial + static_cast<size_t>(blockIdx.x) * D;
   if constexpr (kGroups == 1) {
 #pragma unroll
@@ -447,10 +449,13 @@ cudaError_t launch_layer_norm_fwd(const void* x, DType x_t, const float* w, cons
     constexpr int T = decltype(p)::tpr, N = decltype(p)::ch;
     if (!sh.vec) {
       if constexpr (any_width(T, N)) {
-        ln_fwd_any_kernel<T, N><<<blocks, threads, 0, s>>>(Any{x, x_t == DType::F32}, w, b, eps,
-                                                          invD, AnyOut{y, y_t == DType::F32}, mean, rstd,
-                                                          ntok, D);
-        return cudaGetLastError();
+        return by_type(x_t, [&](auto tx) {
+          using Tx = decltype(tx);
+          ln_fwd_any_kernel<Tx, T, N><<<blocks, threads, 0, s>>>(
+              static_cast<const Tx*>(x), w, b, eps, invD, AnyOut{y, y_t == DType::F32}, mean, rstd,
+              ntok, D);
+          return cudaGetLastError();
+        });
       }
     } else if constexpr (fwd_vec(T, N)) {
       return by_type(x_t, [&](auto tx) {
@@ -484,12 +489,18 @@ cudaError_t launch_layer_norm_bwd(const void* x, DType x_t, const void* dy, DTyp
       const size_t sums = kThreads / T > 1 ? static_cast<size_t>(kThreads / T) * D * sizeof(float) : 0;
       if (!sh.vec) {
         if constexpr (any_width(T, N)) {
-          const cudaError_t a = allow_smem(ln_bwd_any_kernel<T, N>, sums);
-          if (a != cudaSuccess) return a;
-          ln_bwd_any_kernel<T, N><<<blocks, kThreads, sums, s>>>(
-              Any{x, x_t == DType::F32}, Any{dy, dy_t == DType::F32}, mean, rstd, w,
-              AnyOut{dx, dx_t == DType::F32}, part, ntok, D);
-          return cudaGetLastError();
+          return by_type(x_t, [&](auto tx) {
+            return by_type(dy_t, [&](auto tu) {
+              using Tx = decltype(tx);
+              using Tu = decltype(tu);
+              const cudaError_t a = allow_smem(ln_bwd_any_kernel<Tx, Tu, T, N>, sums);
+              if (a != cudaSuccess) return a;
+              ln_bwd_any_kernel<Tx, Tu, T, N><<<blocks, kThreads, sums, s>>>(
+                  static_cast<const Tx*>(x), static_cast<const Tu*>(dy), mean, rstd, w,
+                  AnyOut{dx, dx_t == DType::F32}, part, ntok, D);
+              return cudaGetLastError();
+            });
+          });
         }
       } else if constexpr (bwd_vec(T, N)) {
         return by_type(x_t, [&](auto tx) {

@@ -141,6 +141,7 @@ ng_bwd_kernel(const To* __restrict__ o, const Ti* __restrict__ g, const Ti* __re
     at += stride;
   }
   if (!partial) return;
+  release_dependents();
   float* mine = partial + static_cast<size_t>(first) * token + col;
 #pragma unroll
   for (int k = 0; k < NV; ++k)
@@ -150,11 +151,11 @@ ng_bwd_kernel(const To* __restrict__ o, const Ti* __restrict__ g, const Ti* __re
     }
 }
 
-// Any width, any types: a warp per row, one channel at a time.
-template <int NV>
+// Any width: a warp per row, one channel at a time.
+template <typename To, typename Ti, int NV>
 __global__ void __launch_bounds__(kThreads)
-ng_bwd_any_kernel(Any o, Any g, Any dy, const float* __restrict__ w, const float* __restrict__ b,
-                  float eps, AnyOut d_o, AnyOut d_g, float* __restrict__ partial, int ntok, int H,
+ng_bwd_any_kernel(const To* __restrict__ o, const Ti* __restrict__ g, const Ti* __restrict__ dy,
+                  const float* __restrict__ w, const float* __restrict__ b, float eps, AnyOut d_o, AnyOut d_g, float* __restrict__ partial, int ntok, int H,
                   int dv, int lanes) {
   const int t = threadIdx.x & 31;
   const int group = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -172,9 +173,9 @@ ng_bwd_any_kernel(Any o, Any g, Any dy, const float* __restrict__ w, const float
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = k * 32 + t;
-      ov[k] = c < dv ? o.ld(base + c) : 0.f;
-      gv[k] = c < dv ? g.ld(base + c) : 0.f;
-      uv[k] = c < dv ? dy.ld(base + c) : 0.f;
+      ov[k] = c < dv ? Io<To>::ld(o, base + c) : 0.f;
+      gv[k] = c < dv ? Io<Ti>::ld(g, base + c) : 0.f;
+      uv[k] = c < dv ? Io<Ti>::ld(dy, base + c) : 0.f;
       mean[0] += ov[k];
     }
     row_sum<32>(mean, nullptr, 0);
@@ -208,6 +209,7 @@ ng_bwd_any_kernel(Any o, Any g, Any dy, const float* __restrict__ w, const float
     }
   }
   if (!partial) return;
+  release_dependents();
   float* mine = partial + static_cast<size_t>(first) * token + c0;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
@@ -252,15 +254,22 @@ cudaError_t launch_norm_gate_bwd(const void* o, DType o_t, const void* g, const 
     if (nb > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     const unsigned blocks = static_cast<unsigned>(nb);
     if (dv % 8 != 0) {
-      const Any ao{o, o_t == DType::F32}, ag{g, g_t == DType::F32}, ay{dy, g_t == DType::F32};
       const AnyOut go{d_o, grad_t == DType::F32}, gg{d_g, grad_t == DType::F32};
-      if (dv <= 256)
-        ng_bwd_any_kernel<8><<<blocks, kThreads, 0, s>>>(ao, ag, ay, w, b, eps, go, gg, part, ntok,
-                                                       H, dv, lanes);
-      else
-        ng_bwd_any_kernel<32><<<blocks, kThreads, 0, s>>>(ao, ag, ay, w, b, eps, go, gg, part, ntok,
-                                                        H, dv, lanes);
-      e = cudaGetLastError();
+      e = by_type(o_t, [&](auto to) {
+        return by_type(g_t, [&](auto ti) {
+          using To = decltype(to);
+          using Ti = decltype(ti);
+          const auto run = [&](auto kern) {
+            kern<<<blocks, kThreads, 0, s>>>(static_cast<const To*>(o), static_cast<const Ti*>(g),
+                                             static_cast<const Ti*>(dy), w, b, eps, go, gg, part,
+                                             ntok, H, dv, lanes);
+            return cudaGetLastError();
+          };
+          if (dv <= 128) return run(ng_bwd_any_kernel<To, Ti, 4>);
+          if (dv <= 256) return run(ng_bwd_any_kernel<To, Ti, 8>);
+          return run(ng_bwd_any_kernel<To, Ti, 32>);
+        });
+      });
     } else {
       e = by_type(o_t, [&](auto to) {
         return by_type(g_t, [&](auto ti) {
