@@ -32,6 +32,10 @@ constexpr int kMaxSplit = 16;       // CTAs of a cluster
 // Warps of a CTA, and the consecutive tokens (run) of each.  Long runs share the cost of
 // a round's exchange; the gradients keep three times as much per token in registers.
 constexpr int kFwdWarps = 4, kFwdRun = kTile / kFwdWarps;
+#ifndef FST
+#define FST 2
+#endif
+constexpr int kFwdStages = FST;
 constexpr int kBwdWarps = 8, kBwdRun = kTile / kBwdWarps;
 
 // How a lane's two channels lie and how rows reach shared memory.
@@ -75,11 +79,13 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return y;
 }
 
-__device__ __forceinline__ F2 sigmoid(F2 x) {
-  const F2 n = mul(x, f2(-1.4426950408889634f));
-  const F2 d = add(make_float2(ex2_approx(n.x), ex2_approx(n.y)), f2(1.f));
-  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+// The gates are written for one channel: a packed operation takes four cycles of the FMA pipe
+// for its two results (two single ones take two) and needs its constants in register pairs, while
+// single ones take them as immediates.  Packed operations serve where only registers meet.
+__device__ __forceinline__ float sigmoid(float x) {
+  return rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * x));
 }
+__device__ __forceinline__ F2 sigmoid(F2 x) { return make_float2(sigmoid(x.x), sigmoid(x.y)); }
 
 // a = exp(-y) and root = sqrt(1 - a^2) for y >= 0, both to a few units of their
 // own last place.  y = n ln 2 + g, |g| <= ln 2 / 2, and with w = 1 - e^-g = g + g^2 q(g)
@@ -91,33 +97,35 @@ __device__ __forceinline__ F2 sigmoid(F2 x) {
 // SMALL: y is known to be at most kSmall, so n = 0: the same bits from half the work.
 constexpr float kSmall = 0.3465f;
 template <bool SMALL>
-__device__ __forceinline__ void decay(F2 y, F2& a, F2& root) {
-  F2 g = y, s = f2(1.f);
+__device__ __forceinline__ void decay(float y, float& a, float& root) {
+  float g = y, s = 1.f;
   if constexpr (!SMALL) {
     constexpr float kMagic = 12582912.f;           // 1.5 * 2^23: adding it rounds to an integer
-    y = make_float2(min_nan(y.x, 88.f), min_nan(y.y, 88.f));
-    const F2 m = fma(y, f2(-1.4426950408889634f), f2(kMagic));   // kMagic - n
-    const F2 n = add(m, f2(-kMagic));
-    g = fma(n, f2(0.693147182464599609375f), y);                 // ln 2 in two parts
-    g = fma(n, f2(-1.904654290582768e-9f), g);
-    s = make_float2(__int_as_float((__float_as_int(m.x) << 23) + 0x3f800000),
-                    __int_as_float((__float_as_int(m.y) << 23) + 0x3f800000));
+    y = min_nan(y, 88.f);
+    const float m = fmaf(y, -1.4426950408889634f, kMagic);     // kMagic - n
+    const float n = m - kMagic;
+    g = fmaf(n, 0.693147182464599609375f, y);                  // ln 2 in two parts
+    g = fmaf(n, -1.904654290582768e-9f, g);
+    s = __int_as_float((__float_as_int(m) << 23) + 0x3f800000);
   }
-  F2 w = fma(g, f2(-0.0013945651007816195f), f2(0.008366155438125134f));
-  w = fma(g, w, f2(-0.04166629537940025f));
-  w = fma(g, w, f2(0.1666654795408249f));
-  w = fma(g, w, f2(-0.5f));
-  w = fma(mul(g, g), w, g);
-  F2 below = w;                                    // 1 - a
+  float w = fmaf(g, -0.0013945651007816195f, 0.008366155438125134f);
+  w = fmaf(g, w, -0.04166629537940025f);
+  w = fmaf(g, w, 0.1666654795408249f);
+  w = fmaf(g, w, -0.5f);
+  w = fmaf(g * g, w, g);
+  float below = w;                                 // 1 - a
   if constexpr (SMALL) {
-    a = fma(w, f2(-1.f), f2(1.f));
+    a = 1.f - w;
   } else {
-    const F2 ns = make_float2(-s.x, -s.y);
-    a = fma(ns, w, s);
-    below = fma(s, w, add(ns, f2(1.f)));
+    a = fmaf(-s, w, s);
+    below = fmaf(s, w, 1.f - s);
   }
-  const F2 z = fma(below, a, below);
-  root = make_float2(sqrt_approx(z.x), sqrt_approx(z.y));
+  root = sqrt_approx(fmaf(below, a, below));
+}
+template <bool SMALL>
+__device__ __forceinline__ void decay(F2 y, F2& a, F2& root) {
+  decay<SMALL>(y.x, a.x, root.x);
+  decay<SMALL>(y.y, a.y, root.y);
 }
 
 // ---- sequences and tiles ---------------------------------------------------
@@ -385,7 +393,7 @@ glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ s
   const int S = p.split, rank = static_cast<int>(blockIdx.x % S);
   Exchange& ex = *reinterpret_cast<Exchange*>(smem);
   Maps* cta_maps = reinterpret_cast<Maps*>(smem + sizeof(Exchange));      // [2][S]
-  char* ring = smem + exchange_bytes(S) + warp * (2 * 3 * kArray);
+  char* ring = smem + exchange_bytes(S) + warp * (kFwdStages * 3 * kArray);
   const int pair = static_cast<int>(blockIdx.x / S);
   const int seq = pair / p.groups, c0 = (pair % p.groups) * kChan;
   const int D = p.D;
@@ -405,8 +413,10 @@ glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ s
   const Ti* xp = stage_from<Ti, MODE>(x, first(0), c0, D, lane);
   const Ti* rp = stage_from<Ti, MODE>(r, first(0), c0, D, lane);
   const Ti* ip = stage_from<Ti, MODE>(i, first(0), c0, D, lane);
+  int fill = 0;                         // stage of the next fetch
   const auto fetch = [&](int j) {
-    char* st = ring + (j & 1) * 3 * kArray;
+    char* st = ring + fill * 3 * kArray;
+    fill = fill + 1 == kFwdStages ? 0 : fill + 1;
     if (j < rounds) {
       const int t = first(j);
       stage<Ti, MODE, kRun>(st, x, xp, t, t1, c0, D, total, 0, lane);
@@ -418,17 +428,20 @@ glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ s
     }
     cp_commit();
   };
-  fetch(0);
+#pragma unroll
+  for (int j = 0; j < kFwdStages - 1; ++j) fetch(j);
   const F2 lm = load2(p.lam, 0, cA, cB, D);
   const F2 ysc = make_float2(p.c * softplus(lm.x), p.c * softplus(lm.y));
   F2 carry = load2(state_in, static_cast<size_t>(seq) * D, cA, cB, D);
   exchange_begin(ex, S);
   const auto run = [&](auto small) {
+    int use = 0;
     for (int j = 0; j < rounds; ++j) {
-      fetch(j + 1);
-      cp_wait<1>();
+      fetch(j + kFwdStages - 1);
+      cp_wait<kFwdStages - 1>();
       __syncwarp();
-      const char* st = ring + (j & 1) * 3 * kArray;
+      const char* st = ring + use * 3 * kArray;
+      use = use + 1 == kFwdStages ? 0 : use + 1;
       const int t = first(j);
       F2 a[kRun], v[kRun];
       Map m = identity();
@@ -703,11 +716,9 @@ glr_step_kernel(const Ti* __restrict__ x, const Ti* __restrict__ r, const Ti* __
   const int d = (blockIdx.x % groups) * 128 + threadIdx.x;
   if (d >= D) return;
   const size_t at = static_cast<size_t>(blockIdx.x / groups) * D + d;
-  // one channel: the decay in the pair's first half, the input gate in the sigmoids' second
-  const F2 s = sigmoid(make_float2(Io<Ti>::ld(r, at), Io<Ti>::ld(i, at)));
-  F2 a, root;
-  decay<false>(f2(c * softplus(lam[d]) * s.x), a, root);
-  const float st = fmaf(a.x, state[at], root.x * s.y * Io<Ti>::ld(x, at));
+  float a, root;
+  decay<false>(c * softplus(lam[d]) * sigmoid(Io<Ti>::ld(r, at)), a, root);
+  const float st = fmaf(a, state[at], root * sigmoid(Io<Ti>::ld(i, at)) * Io<Ti>::ld(x, at));
   state_out[at] = st;
   if (h) Io<Th>::st(h, at, st);
 }
@@ -740,6 +751,9 @@ int split_of(const SeqLayout& L, int D) {
   const double pairs = static_cast<double>((D + kChan - 1) / kChan) * L.nseq;
   const long long per = static_cast<long long>(L.nseq) * kTile;
   const long long tiles = (L.Ttot + per - 1) / per;
+#ifdef GLR_SPLIT
+  return GLR_SPLIT;
+#endif
   int best = 1;
   double cost = 0.0;
   for (int s = 1; s <= kMaxSplit && (s == 1 || s <= tiles); ++s) {
@@ -806,7 +820,7 @@ cudaError_t launch_glr_fwd(const void* x, const void* r, const void* i, DType in
         using Ti = decltype(ti);
         using Th = decltype(th);
         constexpr int M = decltype(mode)::value;
-        const size_t smem = exchange_bytes(p.split) + 2 * 3 * kFwdWarps * run_bytes<Ti, M, kFwdRun>();
+        const size_t smem = exchange_bytes(p.split) + kFwdStages * 3 * kFwdWarps * run_bytes<Ti, M, kFwdRun>();
         return launch_split(glr_fwd_kernel<Ti, Th, M>, kFwdWarps * 32, smem, blocks, p.split, s, p, state_in,
                             state_out, static_cast<Th*>(h), chunk_states);
       });
