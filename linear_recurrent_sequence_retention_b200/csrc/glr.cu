@@ -275,6 +275,28 @@ __device__ __forceinline__ F2 row_pair(const char* st, int k, int t, int c0, int
   }
 }
 
+// Two floats per lane in the place of row k of the r array (and, for bf16, of the i array, which
+// follows at `array` bytes).
+template <typename T, int MODE>
+__device__ __forceinline__ void put_state(char* st, int array, int k, int lane, F2 v) {
+  char* row = st + array + k * row_bytes<T, MODE>();
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<float*>(row + lane * 4) = v.x;
+    *reinterpret_cast<float*>(row + array + lane * 4) = v.y;
+  } else {
+    *reinterpret_cast<F2*>(row + lane * 8) = v;
+  }
+}
+template <typename T, int MODE>
+__device__ __forceinline__ F2 get_state(const char* st, int array, int k, int lane) {
+  const char* row = st + array + k * row_bytes<T, MODE>();
+  if constexpr (sizeof(T) == 2)
+    return make_float2(*reinterpret_cast<const float*>(row + lane * 4),
+                       *reinterpret_cast<const float*>(row + array + lane * 4));
+  else
+    return *reinterpret_cast<const F2*>(row + lane * 8);
+}
+
 // `at`: offset of the lane's first channel.
 template <typename T, int MODE>
 __device__ __forceinline__ void store_pair(T* at, F2 v, bool okA, bool okB) {
@@ -635,10 +657,12 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
 #pragma unroll 4
         for (; q >= 0; --q) carry = apply(get(cm[q], lane), carry);
       }
-      F2 hp[kRun];                        // the state before each token
+      // the state before each token, kept where the token's gate inputs were (every lane has read
+      // its own; odd rows share pieces, but all lanes are past the block barrier)
+      char* keep = ring + (j & 1) * kStage;
 #pragma unroll
       for (int k = 0; k < kRun; ++k) {
-        hp[k] = hs;
+        put_state<Ti, MODE>(keep, kArray, k, lane, hs);
         const F2 xv = row_pair<Ti, MODE>(st, k, t + k, c0, D, lane);
         if (k + 1 < kRun) hs = fma(a[k], hs, mul(mul(root[k], si[k]), xv));
       }
@@ -646,17 +670,20 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
 #pragma unroll
       for (int k = kRun - 1; k >= 0; --k) {
         const F2 xv = row_pair<Ti, MODE>(st, k, t + k, c0, D, lane);
+        const F2 hp = get_state<Ti, MODE>(keep, kArray, k, lane);
         const F2 G = add(row_pair<Tu, MODE>(st + 3 * kArray, k, t + k, c0, D, lane), e);
         // 1 / root; where root is zero y is below 1e-38 and y / root counts as zero either way
         const F2 inv = make_float2(rcp_approx(fmaxf(root[k].x, 1e-19f)),
                                    rcp_approx(fmaxf(root[k].y, 1e-19f)));
-        const F2 minus = f2(-1.f);
         const F2 six = mul(si[k], xv);
         const F2 gx = mul(G, mul(root[k], si[k]));
-        const F2 gi = mul(mul(gx, xv), fma(si[k], minus, f2(1.f)));
+        const F2 gix = mul(gx, xv);
+        const F2 gi = make_float2(fmaf(gix.x, -si[k].x, gix.x), fmaf(gix.y, -si[k].y, gix.y));
         e = mul(a[k], G);
-        const F2 u = mul(mul(e, mul(ysc, sr[k])), fma(mul(a[k], inv), six, mul(hp[k], minus)));
-        const F2 gr = mul(u, fma(sr[k], minus, f2(1.f)));
+        const F2 ai = mul(a[k], inv);
+        const F2 u = mul(mul(e, mul(ysc, sr[k])), make_float2(fmaf(ai.x, six.x, -hp.x),
+                                                             fmaf(ai.y, six.y, -hp.y)));
+        const F2 gr = make_float2(fmaf(u.x, -sr[k].x, u.x), fmaf(u.y, -sr[k].y, u.y));
         usum = add(usum, u);
         if (t + k < t1) {
           const size_t o = at + static_cast<size_t>(k) * D;
