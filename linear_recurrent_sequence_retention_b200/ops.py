@@ -8,7 +8,6 @@ is no CPU or PyTorch fallback, and calling any function without the built
 library raises immediately.
 """
 
-import contextlib
 import ctypes
 import os
 
@@ -647,24 +646,45 @@ def norm_gate(o, g, weight=None, bias=None, eps=1e-5, out_dtype=None, out=None, 
 
 def _ready(stream, **tensors):
     """Checks the tensors of one call (None allowed): contiguous CUDA tensors, all on the
-    current device, as is ``stream``."""
-    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
+    current device, as is ``stream``.  Returns the raw stream to launch on."""
+    cur = None
     for name, t in tensors.items():
-        if t is not None:
+        if t is None:
+            continue
+        if cur is None:
             _dev(t, name)
-            if t.device.index != cur:
-                raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
-    if stream is not None and stream.device.index != cur:
+            cur = torch.cuda.current_device()
+        if not (isinstance(t, torch.Tensor) and t.is_contiguous() and t.get_device() == cur):
+            _dev(t, name)
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+    if stream is None:
+        return _current_raw_stream(cur)
+    if stream.device.index != cur:
         raise ValueError(f"stream is on {stream.device}, the current device is cuda:{cur}")
+    return stream.cuda_stream
 
 
-def _alloc_on(stream):
-    """Context in which new tensors belong to the stream the kernels will run on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _current_raw_stream(device):
+    # the stream as an integer, without building a Stream object (3 us of a 10 us call)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream().cuda_stream if raw is None else raw(device)
+
+
+def _new(stream, shape, dtype, like):
+    """An uninitialised tensor that belongs to the stream the kernels will run on."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _at(t):
+    """Device address as the integer ctypes takes for a pointer."""
+    return None if t is None else t.data_ptr()
 
 
 def _shaped(t, name, shape, dtype=None):
-    if t is not None and (tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype)):
+    if t is not None and (t.shape != shape or (dtype is not None and t.dtype != dtype)):
         kind = "" if dtype is None else f"{str(dtype)[6:]} "
         raise ValueError(f"{name} must be {kind}{list(shape)}")
 
@@ -704,8 +724,8 @@ def glr_fwd(x, r, i, lam, c=8.0, cu_seqlens=None, state_in=None, return_state=Fa
     ``h`` [B,T,D], then the final states with ``return_state``, then with ``return_chunks``
     the states entering every 64 tokens (float32 [slots,D]), which :func:`glr_bwd` takes.
     """
-    _ready(stream, x=x, r=r, i=i, lam=lam, cu_seqlens=cu_seqlens, state_in=state_in, out=out,
-           state_out=state_out, chunk_states=chunk_states)
+    raw = _ready(stream, x=x, r=r, i=i, lam=lam, cu_seqlens=cu_seqlens, state_in=state_in, out=out,
+                 state_out=state_out, chunk_states=chunk_states)
     B, T, D, nseq = _glr_inputs(x, r, i, lam, cu_seqlens)
     states = (nseq or B, D)
     slots = (glr_chunk_slots(B, T, nseq), D) if return_chunks or chunk_states is not None else None
@@ -713,17 +733,15 @@ def glr_fwd(x, r, i, lam, c=8.0, cu_seqlens=None, state_in=None, return_state=Fa
     _shaped(state_out, "state_out", states, torch.float32)
     _shaped(out, "out", x.shape, out_dtype)
     _shaped(chunk_states, "chunk_states", slots, torch.float32)
-    with _alloc_on(stream):
-        if out is None:
-            out = torch.empty(x.shape, device=x.device, dtype=out_dtype or x.dtype)
-        if return_state and state_out is None:
-            state_out = torch.empty(states, device=x.device, dtype=torch.float32)
-        if return_chunks and chunk_states is None:
-            chunk_states = torch.empty(slots, device=x.device, dtype=torch.float32)
-    st = lib().retention_glr_fwd(_ptr(x), _ptr(r), _ptr(i), _dt(x), _ptr(lam), float(c),
-                                 _ptr(cu_seqlens), nseq, _ptr(state_in), _ptr(state_out),
-                                 _ptr(out), _dt(out), _ptr(chunk_states), B, T, D,
-                                 _stream(stream))
+    if out is None:
+        out = _new(stream, x.shape, out_dtype or x.dtype, x)
+    if return_state and state_out is None:
+        state_out = _new(stream, states, torch.float32, x)
+    if return_chunks and chunk_states is None:
+        chunk_states = _new(stream, slots, torch.float32, x)
+    st = lib().retention_glr_fwd(_at(x), _at(r), _at(i), _dt(x), _at(lam), float(c),
+                                 _at(cu_seqlens), nseq, _at(state_in), _at(state_out), _at(out),
+                                 _dt(out), _at(chunk_states), B, T, D, raw)
     _check(st, "retention_glr_fwd")
     if not (return_state or return_chunks):
         return out
@@ -744,27 +762,25 @@ def glr_bwd(x, r, i, lam, chunk_states, d_h, c=8.0, cu_seqlens=None, d_state_out
     ``(dx, dr, di, d_lam)``, the first three in ``grad_dtype`` (default: x's dtype), and with
     ``return_d_state`` the gradient of the initial states.
     """
-    _ready(stream, x=x, r=r, i=i, lam=lam, chunk_states=chunk_states, d_h=d_h,
-           cu_seqlens=cu_seqlens, d_state_out=d_state_out, workspace=workspace)
+    raw = _ready(stream, x=x, r=r, i=i, lam=lam, chunk_states=chunk_states, d_h=d_h,
+                 cu_seqlens=cu_seqlens, d_state_out=d_state_out, workspace=workspace)
     B, T, D, nseq = _glr_inputs(x, r, i, lam, cu_seqlens)
     states = (nseq or B, D)
     _shaped(d_h, "d_h", x.shape)
     _shaped(chunk_states, "chunk_states", (glr_chunk_slots(B, T, nseq), D), torch.float32)
     _shaped(d_state_out, "d_state_out", states, torch.float32)
     need = glr_bwd_workspace_size(B, T, D, nseq)
-    with _alloc_on(stream):
-        dx, dr, di = (torch.empty(x.shape, device=x.device, dtype=grad_dtype or x.dtype)
-                      for _ in range(3))
-        d_lam = torch.empty(D, device=x.device, dtype=torch.float32)
-        dS = torch.empty(states, device=x.device, dtype=torch.float32) if return_d_state else None
-        if workspace is None:
-            workspace = alloc_workspace(need, x.device)
-    st = lib().retention_glr_bwd(_ptr(x), _ptr(r), _ptr(i), _dt(x), _ptr(lam), float(c),
-                                 _ptr(cu_seqlens), nseq, _ptr(chunk_states), _ptr(d_h), _dt(d_h),
-                                 _ptr(d_state_out), _ptr(dx), _ptr(dr), _ptr(di), _dt(dx),
-                                 _ptr(d_lam), _ptr(dS), _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), B, T, D,
-                                 _stream(stream))
+    gd = grad_dtype or x.dtype
+    dx, dr, di = (_new(stream, x.shape, gd, x) for _ in range(3))
+    d_lam = _new(stream, (D,), torch.float32, x)
+    dS = _new(stream, states, torch.float32, x) if return_d_state else None
+    if workspace is None:
+        workspace = _new(stream, (need,), torch.uint8, x)
+    st = lib().retention_glr_bwd(_at(x), _at(r), _at(i), _dt(x), _at(lam), float(c),
+                                 _at(cu_seqlens), nseq, _at(chunk_states), _at(d_h), _dt(d_h),
+                                 _at(d_state_out), _at(dx), _at(dr), _at(di), _dt(dx), _at(d_lam),
+                                 _at(dS), _at(workspace),
+                                 workspace.numel() * workspace.element_size(), B, T, D, raw)
     _check(st, "retention_glr_bwd")
     return (dx, dr, di, d_lam, dS) if return_d_state else (dx, dr, di, d_lam)
 
@@ -773,7 +789,7 @@ def glr_step(x, r, i, lam, state, c=8.0, out_dtype=torch.float32, out=None, stat
              stream=None):
     """One token of the gated linear recurrence for N sequences: x, r, i [N,D], ``state``
     float32 [N,D], updated in place unless ``state_out`` is given.  Returns h [N,D]."""
-    _ready(stream, x=x, r=r, i=i, lam=lam, state=state, out=out, state_out=state_out)
+    raw = _ready(stream, x=x, r=r, i=i, lam=lam, state=state, out=out, state_out=state_out)
     if x.dim() != 2 or r.shape != x.shape or i.shape != x.shape or not x.dtype == r.dtype == i.dtype:
         raise ValueError("x, r, i must have one [N,D] shape and one dtype")
     N, D = x.shape
@@ -782,13 +798,11 @@ def glr_step(x, r, i, lam, state, c=8.0, out_dtype=torch.float32, out=None, stat
     _shaped(state_out, "state_out", (N, D), torch.float32)
     _shaped(out, "out", (N, D))
     if out is None:
-        with _alloc_on(stream):
-            out = torch.empty(N, D, device=x.device, dtype=out_dtype)
+        out = _new(stream, (N, D), out_dtype, x)
     if state_out is None:
         state_out = state
-    st = lib().retention_glr_step(_ptr(x), _ptr(r), _ptr(i), _dt(x), _ptr(lam), float(c),
-                                  _ptr(state), _ptr(state_out), _ptr(out), _dt(out), N, D,
-                                  _stream(stream))
+    st = lib().retention_glr_step(_at(x), _at(r), _at(i), _dt(x), _at(lam), float(c), _at(state),
+                                  _at(state_out), _at(out), _dt(out), N, D, raw)
     _check(st, "retention_glr_step")
     return out
 
@@ -798,7 +812,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out_dtype=None, out=None
     """Layer norm over the last dimension (retention_layer_norm_fwd); x: [...,D], weight and
     bias: float32 [D] or None.  Returns y and, with ``return_stats``, the float32 mean and
     1/sqrt(var + eps) of every row, which :func:`layer_norm_bwd` takes."""
-    _ready(stream, x=x, weight=weight, bias=bias, out=out)
+    raw = _ready(stream, x=x, weight=weight, bias=bias, out=out)
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must have a last dimension to normalise")
     D = x.shape[-1]
@@ -807,15 +821,12 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out_dtype=None, out=None
     _shaped(bias, "bias", (D,), torch.float32)
     _shaped(out, "out", x.shape, out_dtype)
     mean = rstd = None
-    with _alloc_on(stream):
-        if out is None:
-            out = torch.empty(x.shape, device=x.device, dtype=out_dtype or x.dtype)
-        if return_stats:
-            mean = torch.empty(x.shape[:-1], device=x.device, dtype=torch.float32)
-            rstd = torch.empty(x.shape[:-1], device=x.device, dtype=torch.float32)
-    st = lib().retention_layer_norm_fwd(_ptr(x), _dt(x), _ptr(weight), _ptr(bias), float(eps),
-                                        _ptr(out), _dt(out), _ptr(mean), _ptr(rstd), ntok, D,
-                                        _stream(stream))
+    if out is None:
+        out = _new(stream, x.shape, out_dtype or x.dtype, x)
+    if return_stats:
+        mean, rstd = (_new(stream, x.shape[:-1], torch.float32, x) for _ in range(2))
+    st = lib().retention_layer_norm_fwd(_at(x), _dt(x), _at(weight), _at(bias), float(eps),
+                                        _at(out), _dt(out), _at(mean), _at(rstd), ntok, D, raw)
     _check(st, "retention_layer_norm_fwd")
     return (out, mean, rstd) if return_stats else out
 
@@ -829,7 +840,7 @@ def layer_norm_bwd(x, d_y, mean, rstd, weight=None, return_d_affine=True, grad_d
     """Gradients of :func:`layer_norm_fwd` (retention_layer_norm_bwd); ``mean`` and ``rstd`` as
     the forward returned them.  Returns ``(dx, d_weight, d_bias)`` (dx in ``grad_dtype``,
     default x's; the others float32 [D]), or dx alone without ``return_d_affine``."""
-    _ready(stream, x=x, d_y=d_y, mean=mean, rstd=rstd, weight=weight, workspace=workspace)
+    raw = _ready(stream, x=x, d_y=d_y, mean=mean, rstd=rstd, weight=weight, workspace=workspace)
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must have a last dimension to normalise")
     D = x.shape[-1]
@@ -839,18 +850,15 @@ def layer_norm_bwd(x, d_y, mean, rstd, weight=None, return_d_affine=True, grad_d
     _shaped(rstd, "rstd", x.shape[:-1], torch.float32)
     _shaped(weight, "weight", (D,), torch.float32)
     dw = db = None
-    with _alloc_on(stream):
-        dx = torch.empty(x.shape, device=x.device, dtype=grad_dtype or x.dtype)
-        if return_d_affine:
-            dw = torch.empty(D, device=x.device, dtype=torch.float32)
-            db = torch.empty(D, device=x.device, dtype=torch.float32)
-            if workspace is None:
-                workspace = alloc_workspace(layer_norm_bwd_workspace_size(ntok, D), x.device)
+    dx = _new(stream, x.shape, grad_dtype or x.dtype, x)
+    if return_d_affine:
+        dw, db = (_new(stream, (D,), torch.float32, x) for _ in range(2))
+        if workspace is None:
+            workspace = _new(stream, (layer_norm_bwd_workspace_size(ntok, D),), torch.uint8, x)
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    st = lib().retention_layer_norm_bwd(_ptr(x), _dt(x), _ptr(d_y), _dt(d_y), _ptr(mean),
-                                        _ptr(rstd), _ptr(weight), _ptr(dx), _dt(dx), _ptr(dw),
-                                        _ptr(db), _ptr(workspace), nbytes, ntok, D,
-                                        _stream(stream))
+    st = lib().retention_layer_norm_bwd(_at(x), _dt(x), _at(d_y), _dt(d_y), _at(mean), _at(rstd),
+                                        _at(weight), _at(dx), _dt(dx), _at(dw), _at(db),
+                                        _at(workspace), nbytes, ntok, D, raw)
     _check(st, "retention_layer_norm_bwd")
     return (dx, dw, db) if return_d_affine else dx
 
@@ -865,7 +873,7 @@ def norm_gate_bwd(o, g, d_y, weight=None, bias=None, eps=1e-5, return_d_affine=T
     size and d_y's dtype.  Returns ``(d_o, d_g, d_weight, d_bias)``: the first two in
     ``grad_dtype`` (default d_y's) and shaped as o and g, the others float32 [H*dv] and left
     out without ``return_d_affine``.  d_o is the ``d_out`` of :func:`chunkwise_bwd`."""
-    _ready(stream, o=o, g=g, d_y=d_y, weight=weight, bias=bias, workspace=workspace)
+    raw = _ready(stream, o=o, g=g, d_y=d_y, weight=weight, bias=bias, workspace=workspace)
     if o.dim() < 2 or min(o.shape[-2:]) < 1:
         raise ValueError("o must be [...,H,dv]")
     H, dv = o.shape[-2], o.shape[-1]
@@ -877,20 +885,18 @@ def norm_gate_bwd(o, g, d_y, weight=None, bias=None, eps=1e-5, return_d_affine=T
         if t is not None and (t.dtype != torch.float32 or t.numel() != H * dv):
             raise ValueError(f"{n} must be float32 with H*dv elements")
     dw = db = None
-    with _alloc_on(stream):
-        d_o = torch.empty(o.shape, device=o.device, dtype=grad_dtype or d_y.dtype)
-        d_g = torch.empty(g.shape, device=o.device, dtype=grad_dtype or d_y.dtype)
-        if return_d_affine:
-            dw = torch.empty(H * dv, device=o.device, dtype=torch.float32)
-            db = torch.empty(H * dv, device=o.device, dtype=torch.float32)
-            if workspace is None:
-                workspace = alloc_workspace(norm_gate_bwd_workspace_size(ntok, H, dv), o.device)
+    gd = grad_dtype or d_y.dtype
+    d_o, d_g = _new(stream, o.shape, gd, o), _new(stream, g.shape, gd, o)
+    if return_d_affine:
+        dw, db = (_new(stream, (H * dv,), torch.float32, o) for _ in range(2))
+        if workspace is None:
+            workspace = _new(stream, (norm_gate_bwd_workspace_size(ntok, H, dv),), torch.uint8,
+                             o)
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    ng = NormGate(g.data_ptr(), _dt(g), weight.data_ptr() if weight is not None else None,
-                  bias.data_ptr() if bias is not None else None, float(eps))
-    st = lib().msr_norm_gate_bwd(_ptr(o), _dt(o), ctypes.byref(ng), _ptr(d_y), _ptr(d_o),
-                                 _ptr(d_g), _dt(d_o), _ptr(dw), _ptr(db), _ptr(workspace), nbytes,
-                                 ntok, H, dv, _stream(stream))
+    ng = NormGate(g.data_ptr(), _dt(g), _at(weight), _at(bias), float(eps))
+    st = lib().msr_norm_gate_bwd(_at(o), _dt(o), ctypes.byref(ng), _at(d_y), _at(d_o), _at(d_g),
+                                 _dt(d_o), _at(dw), _at(db), _at(workspace), nbytes, ntok, H, dv,
+                                 raw)
     _check(st, "msr_norm_gate_bwd")
     return (d_o, d_g, dw, db) if return_d_affine else (d_o, d_g)
 

@@ -158,18 +158,27 @@ def test_binding_refuses_host_tensors():
         ops.layer_norm_fwd([1.0])
 
 
-class _Elsewhere:
+class _Elsewhere(torch.Tensor):
     """Stands in for a tensor on a device that is not the current one."""
 
     device = torch.device("cuda:7")
+
+    def get_device(self):
+        return 7
+
+
+class _Here(_Elsewhere):
+    def get_device(self):
+        return 0
 
 
 def test_binding_refuses_another_device(monkeypatch):
     ops, _ = _lib()
     monkeypatch.setattr(ops, "_dev", lambda t, name: t)
-    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with pytest.raises(ValueError, match="x is on cuda:7, the current device is cuda:0"):
         ops._ready(None, x=_Elsewhere())
+    with pytest.raises(ValueError, match="y is on cuda:7, the current device is cuda:0"):
+        ops._ready(None, x=_Here(), y=_Elsewhere())
     with pytest.raises(ValueError, match="stream is on cuda:7"):
-        ops._ready(_Elsewhere(), x=None)
+        ops._ready(_Elsewhere(), x=_Here())
