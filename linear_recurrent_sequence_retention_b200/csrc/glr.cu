@@ -535,6 +535,19 @@ glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ s
 
 // ---- gradients -------------------------------------------------------------
 
+// A token's gradients from G = d_h + e, the e it passes on (a G) and the state before it.
+__device__ __forceinline__ void gate_gradients(F2 G, F2 e, F2 a, F2 root, F2 y, F2 sr, F2 si, F2 x,
+                                               F2 hp, F2& gx, F2& gr, F2& gi, F2& u) {
+  // 1 / root; where root is zero y is below 1e-38 and y / root counts as zero either way
+  const F2 inv = make_float2(rcp_approx(fmaxf(root.x, 1e-19f)), rcp_approx(fmaxf(root.y, 1e-19f)));
+  const F2 six = mul(si, x), ai = mul(a, inv);
+  gx = mul(G, mul(root, si));
+  const F2 gix = mul(gx, x);
+  gi = make_float2(fmaf(gix.x, -si.x, gix.x), fmaf(gix.y, -si.y, gix.y));
+  u = mul(mul(e, y), make_float2(fmaf(ai.x, six.x, -hp.x), fmaf(ai.y, six.y, -hp.y)));
+  gr = make_float2(fmaf(u.x, -sr.x, u.x), fmaf(u.y, -sr.y, u.y));
+}
+
 template <typename Ti, typename Tu, typename Tg, int MODE>
 __global__ void __launch_bounds__(kBwdWarps * 32, 2)
 glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restrict__ dh,
@@ -672,18 +685,9 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
         const F2 xv = row_pair<Ti, MODE>(st, k, t + k, c0, D, lane);
         const F2 hp = get_state<Ti, MODE>(keep, kArray, k, lane);
         const F2 G = add(row_pair<Tu, MODE>(st + 3 * kArray, k, t + k, c0, D, lane), e);
-        // 1 / root; where root is zero y is below 1e-38 and y / root counts as zero either way
-        const F2 inv = make_float2(rcp_approx(fmaxf(root[k].x, 1e-19f)),
-                                   rcp_approx(fmaxf(root[k].y, 1e-19f)));
-        const F2 six = mul(si[k], xv);
-        const F2 gx = mul(G, mul(root[k], si[k]));
-        const F2 gix = mul(gx, xv);
-        const F2 gi = make_float2(fmaf(gix.x, -si[k].x, gix.x), fmaf(gix.y, -si[k].y, gix.y));
+        F2 gx, gr, gi, u;
         e = mul(a[k], G);
-        const F2 ai = mul(a[k], inv);
-        const F2 u = mul(mul(e, mul(ysc, sr[k])), make_float2(fmaf(ai.x, six.x, -hp.x),
-                                                             fmaf(ai.y, six.y, -hp.y)));
-        const F2 gr = make_float2(fmaf(u.x, -sr[k].x, u.x), fmaf(u.y, -sr[k].y, u.y));
+        gate_gradients(G, e, a[k], root[k], mul(ysc, sr[k]), sr[k], si[k], xv, hp, gx, gr, gi, u);
         usum = add(usum, u);
         if (t + k < t1) {
           const size_t o = at + static_cast<size_t>(k) * D;
@@ -711,6 +715,166 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
     store2(partial, (static_cast<size_t>(seq) * S + rank) * D, usum, cA, cB, D);
   }
   exchange_end(S);
+}
+
+// ---- short sequences ------------------------------------------------------------
+//
+// A thread takes two channels of one sequence through time, and nothing is exchanged.  Eight tokens
+// are loaded at a time.
+
+constexpr int kDirectThreads = 128, kDirectChan = 2 * kDirectThreads, kBatch = 8;
+
+// Two channels of a row: adjacent (PAIR), or kDirectThreads apart.
+template <typename T, bool PAIR>
+__device__ __forceinline__ F2 load_two(const T* row, bool okA, bool okB) {
+  if constexpr (PAIR) {
+    if (!okA) return f2(0.f);
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(row));
+      return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    } else {
+      return __ldg(reinterpret_cast<const F2*>(row));
+    }
+  } else {
+    return make_float2(okA ? Io<T>::ld(row, 0) : 0.f, okB ? Io<T>::ld(row, kDirectThreads) : 0.f);
+  }
+}
+template <typename T, bool PAIR>
+__device__ __forceinline__ void store_two(T* row, F2 v, bool okA, bool okB) {
+  if constexpr (PAIR) {
+    if (!okA) return;
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<__nv_bfloat162*>(row) = __floats2bfloat162_rn(v.x, v.y);
+    else
+      *reinterpret_cast<F2*>(row) = v;
+  } else {
+    if (okA) Io<T>::st(row, 0, v.x);
+    if (okB) Io<T>::st(row, kDirectThreads, v.y);
+  }
+}
+
+template <typename Ti, typename Th, bool PAIR>
+__global__ void __launch_bounds__(kDirectThreads)
+glr_fwd_direct_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ state_out,
+                      Th* __restrict__ h, float* __restrict__ chunk_states) {
+  const int D = p.D;
+  const int seq = static_cast<int>(blockIdx.x / p.groups), c0 = static_cast<int>(blockIdx.x % p.groups) * kDirectChan;
+  const int cA = c0 + (PAIR ? 2 : 1) * static_cast<int>(threadIdx.x), cB = cA + (PAIR ? 1 : kDirectThreads);
+  const bool okA = cA < D, okB = cB < D;
+  if (c0 == 0 && threadIdx.x == 0) check_offsets(p.L, seq, p.err);
+  if (!okA) return;
+  int t0, t1;
+  seq_bounds(p.L, seq, t0, t1);
+  const F2 lm = load2(p.lam, 0, cA, cB, D);
+  const F2 ysc = make_float2(p.c * softplus(lm.x), p.c * softplus(lm.y));
+  F2 st = load2(state_in, static_cast<size_t>(seq) * D, cA, cB, D);
+  size_t at = static_cast<size_t>(t0) * D + cA;
+  for (int t = t0; t < t1; t += kBatch) {
+    F2 x[kBatch], r[kBatch], i[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const bool in = t + k < t1;
+      const size_t o = at + static_cast<size_t>(k) * D;
+      x[k] = load_two<Ti, PAIR>(static_cast<const Ti*>(p.x) + o, in, in && okB);
+      r[k] = load_two<Ti, PAIR>(static_cast<const Ti*>(p.r) + o, in, in && okB);
+      i[k] = load_two<Ti, PAIR>(static_cast<const Ti*>(p.i) + o, in, in && okB);
+    }
+    if (chunk_states && (t - t0) % kGlrChunk == 0)
+      store2(chunk_states, static_cast<size_t>(chunk_row(t0, seq) + (t - t0) / kGlrChunk) * D, st, cA,
+             cB, D);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (t + k >= t1) break;
+      F2 a, root;
+      decay<false>(mul(ysc, sigmoid(r[k])), a, root);
+      st = fma(a, st, mul(mul(root, sigmoid(i[k])), x[k]));
+      store_two<Th, PAIR>(h + at + static_cast<size_t>(k) * D, st, true, okB);
+    }
+    at += static_cast<size_t>(kBatch) * D;
+  }
+  if (state_out) store2(state_out, static_cast<size_t>(seq) * D, st, cA, cB, D);
+}
+
+// The chunk's states at every eighth token are formed first; then its batches, last to first.
+template <typename Ti, typename Tu, typename Tg, bool PAIR>
+__global__ void __launch_bounds__(kDirectThreads)
+glr_bwd_direct_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restrict__ dh,
+                      const float* __restrict__ d_state_out, Tg* __restrict__ dx,
+                      Tg* __restrict__ dr, Tg* __restrict__ di, float* __restrict__ d_state_in,
+                      float* __restrict__ partial) {
+  const int D = p.D;
+  const int seq = static_cast<int>(blockIdx.x / p.groups), c0 = static_cast<int>(blockIdx.x % p.groups) * kDirectChan;
+  const int cA = c0 + (PAIR ? 2 : 1) * static_cast<int>(threadIdx.x), cB = cA + (PAIR ? 1 : kDirectThreads);
+  const bool okA = cA < D, okB = cB < D;
+  if (c0 == 0 && threadIdx.x == 0) check_offsets(p.L, seq, p.err);
+  if (!okA) return;
+  const Ti* x = static_cast<const Ti*>(p.x);
+  const Ti* r = static_cast<const Ti*>(p.r);
+  const Ti* i = static_cast<const Ti*>(p.i);
+  int t0, t1;
+  seq_bounds(p.L, seq, t0, t1);
+  const F2 lm = load2(p.lam, 0, cA, cB, D);
+  const F2 ysc = make_float2(p.c * softplus(lm.x), p.c * softplus(lm.y));
+  const size_t so = static_cast<size_t>(seq) * D;
+  F2 e = load2(d_state_out, so, cA, cB, D), usum = f2(0.f);
+  F2 enter[kGlrChunk / kBatch];           // the state before each batch of the chunk
+  for (int ch = ceil_div(t1 - t0, kGlrChunk) - 1; ch >= 0; --ch) {
+    const int first = t0 + ch * kGlrChunk, end = min(first + kGlrChunk, t1);
+    const int batches = ceil_div(end - first, kBatch);
+    F2 st = load2(chunk_states, static_cast<size_t>(chunk_row(t0, seq) + ch) * D, cA, cB, D);
+    for (int b = 0; b < batches; ++b) {
+      enter[b] = st;
+      if (b + 1 == batches) break;
+      const size_t at = static_cast<size_t>(first + b * kBatch) * D + cA;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const size_t o = at + static_cast<size_t>(k) * D;
+        F2 a, root;
+        decay<false>(mul(ysc, sigmoid(load_two<Ti, PAIR>(r + o, true, okB))), a, root);
+        st = fma(a, st, mul(mul(root, sigmoid(load_two<Ti, PAIR>(i + o, true, okB))),
+                            load_two<Ti, PAIR>(x + o, true, okB)));
+      }
+    }
+    for (int b = batches - 1; b >= 0; --b) {
+      const int t = first + b * kBatch;
+      const size_t at = static_cast<size_t>(t) * D + cA;
+      F2 xv[kBatch], uv[kBatch], a[kBatch], root[kBatch], sr[kBatch], si[kBatch], hp[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const bool in = t + k < end;
+        const size_t o = at + static_cast<size_t>(k) * D;
+        xv[k] = load_two<Ti, PAIR>(x + o, in, in && okB);
+        sr[k] = load_two<Ti, PAIR>(r + o, in, in && okB);
+        si[k] = load_two<Ti, PAIR>(i + o, in, in && okB);
+        uv[k] = load_two<Tu, PAIR>(dh + o, in, in && okB);
+      }
+      F2 hs = enter[b];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        sr[k] = sigmoid(sr[k]);
+        si[k] = sigmoid(si[k]);
+        decay<false>(mul(ysc, sr[k]), a[k], root[k]);
+        hp[k] = hs;
+        hs = fma(a[k], hs, mul(mul(root[k], si[k]), xv[k]));
+      }
+#pragma unroll
+      for (int k = kBatch - 1; k >= 0; --k) {
+        if (t + k >= end) continue;
+        const F2 G = add(uv[k], e);
+        F2 gx, gr, gi, u;
+        e = mul(a[k], G);
+        gate_gradients(G, e, a[k], root[k], mul(ysc, sr[k]), sr[k], si[k], xv[k], hp[k], gx, gr, gi,
+                       u);
+        usum = add(usum, u);
+        const size_t o = at + static_cast<size_t>(k) * D;
+        store_two<Tg, PAIR>(dx + o, gx, true, okB);
+        store_two<Tg, PAIR>(dr + o, gr, true, okB);
+        store_two<Tg, PAIR>(di + o, gi, true, okB);
+      }
+    }
+  }
+  if (d_state_in) store2(d_state_in, so, e, cA, cB, D);
+  store2(partial, so, usum, cA, cB, D);
 }
 
 // d_lam = (sum of the partial rows) sigmoid(lam) / softplus(lam).  32 channels
@@ -773,14 +937,11 @@ cudaError_t by_mode(DType in_t, int D, F&& f) {
 // Packed sequences differ in length: the SMs share the average and the longest, taken as four
 // times the average, ends last (64 sequences, 200000 tokens x 1024: S = 1: 0.581, 4: 0.440,
 // 16: 0.625).
+constexpr double kSms = 148.0;
 int split_of(const SeqLayout& L, int D) {
-  constexpr double kSms = 148.0;
   const double pairs = static_cast<double>((D + kChan - 1) / kChan) * L.nseq;
   const long long per = static_cast<long long>(L.nseq) * kTile;
   const long long tiles = (L.Ttot + per - 1) / per;
-#ifdef GLR_SPLIT
-  return GLR_SPLIT;
-#endif
   int best = 1;
   double cost = 0.0;
   for (int s = 1; s <= kMaxSplit && (s == 1 || s <= tiles); ++s) {
@@ -799,6 +960,14 @@ int split_of(const SeqLayout& L, int D) {
     }
   }
   return best;
+}
+
+// Whether threads walk their sequences alone: up to 32 tokens per sequence (16 on average where the
+// lengths differ, which the host does not know).  Measured in us, forward / gradients, alone and by
+// tiles: 256 x 4 x 4096 bf16 15 / 32 and 130 / 253, 32 x 16 x 2048 6.0 / 9.6 and 10.9 / 20.9, 128 x 64 x
+// 4096 77 / 196 and 74 / 169.
+bool direct(const SeqLayout& L) {
+  return L.Ttot <= (L.T > 0 ? 32ll : 16ll) * L.nseq;
 }
 
 // Fills the common arguments and launches `kern` on clusters of `split` CTAs.
@@ -831,7 +1000,7 @@ cudaError_t launch_split(void (*kern)(P...), int threads, size_t smem, long long
 }  // namespace
 
 long long glr_bwd_partial_rows(const SeqLayout& L, int D) {
-  return static_cast<long long>(L.nseq) * split_of(L, D);
+  return static_cast<long long>(L.nseq) * (direct(L) ? 1 : split_of(L, D));
 }
 
 cudaError_t launch_glr_fwd(const void* x, const void* r, const void* i, DType in_t,
@@ -840,9 +1009,23 @@ cudaError_t launch_glr_fwd(const void* x, const void* r, const void* i, DType in
                            unsigned* err, cudaStream_t s) {
   Args p{x, r, i, lam, c, L, D, (D + kChan - 1) / kChan,
          split_of(L, D), err};
+  const bool alone = direct(L);
+  if (alone) {
+    p.groups = (D + kDirectChan - 1) / kDirectChan;
+    p.split = 1;
+  }
   const long long blocks = static_cast<long long>(p.groups) * L.nseq * p.split;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   return by_type(in_t, [&](auto ti) {
     return by_type(h_t, [&](auto th) {
+      if (alone) {
+        using Ti = decltype(ti);
+        using Th = decltype(th);
+        auto kern = D % 2 == 0 ? glr_fwd_direct_kernel<Ti, Th, true> : glr_fwd_direct_kernel<Ti, Th, false>;
+        kern<<<static_cast<unsigned>(blocks), kDirectThreads, 0, s>>>(p, state_in, state_out,
+                                                                       static_cast<Th*>(h), chunk_states);
+        return cudaGetLastError();
+      }
       return by_mode(in_t, D, [&](auto mode) {
         using Ti = decltype(ti);
         using Th = decltype(th);
@@ -863,10 +1046,26 @@ cudaError_t launch_glr_bwd(const void* x, const void* r, const void* i, DType in
                            cudaStream_t s) {
   Args p{x, r, i, lam, c, L, D, (D + kChan - 1) / kChan,
          split_of(L, D), err};
+  const bool alone = direct(L);
+  if (alone) {
+    p.groups = (D + kDirectChan - 1) / kDirectChan;
+    p.split = 1;
+  }
   const long long blocks = static_cast<long long>(p.groups) * L.nseq * p.split;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   const cudaError_t e = by_type(in_t, [&](auto ti) {
     return by_type(dh_t, [&](auto tu) {
       return by_type(g_t, [&](auto tg) {
+        if (alone) {
+          using Ti = decltype(ti);
+          using Tu = decltype(tu);
+          using Tg = decltype(tg);
+          auto kern = D % 2 == 0 ? glr_bwd_direct_kernel<Ti, Tu, Tg, true> : glr_bwd_direct_kernel<Ti, Tu, Tg, false>;
+          kern<<<static_cast<unsigned>(blocks), kDirectThreads, 0, s>>>(
+              p, chunk_states, static_cast<const Tu*>(d_h), d_state_out, static_cast<Tg*>(dx),
+              static_cast<Tg*>(dr), static_cast<Tg*>(di), d_state_in, partial);
+          return cudaGetLastError();
+        }
         return by_mode(in_t, D, [&](auto mode) {
           using Ti = decltype(ti);
           using Tu = decltype(tu);
