@@ -5,18 +5,25 @@
 //
 // A token is the affine map h -> a h + v (v = b x), and a run of tokens is one
 // too: (A, V) then (a, v) is (a A, a V + v).  So time is split: a CTA takes 64
-// channels and 64 tokens, a warp 8 of those tokens, and a cluster of S CTAs 64 S
-// consecutive tokens per round.  Every warp forms the map of its 8 tokens from
-// registers, the maps of the CTA's 8 warps meet in shared memory and those of
-// the cluster's CTAs through distributed shared memory (one cluster barrier per
-// round); each warp then applies its tokens to the state that enters them.
+// channels and 64 tokens per round, a warp 16 (gradients: 8) of those tokens, and
+// a cluster of S CTAs 64 S consecutive tokens.  Every warp forms the map of its
+// run from registers, the maps of the CTA's runs meet in shared memory and those
+// of the cluster's CTAs are sent to each other's shared memory (st.async on an
+// mbarrier); each warp then applies its tokens to the state that enters them.
 // Every input is read from HBM once and every output written once.  The
 // gradients run the same scheme from the last round to the first on
 // e -> a (dh + e), with the forward's states formed again from the state that
-// enters each 64-token tile, which the forward stored.
+// enters each 64-token tile, which the forward stored.  The inputs of the next
+// round are copied to shared memory (cp.async) while the current one is computed.
 //
-// The inputs of the next round are copied to shared memory (cp.async) while the
-// current one is computed.
+// Measured at 2 x 8192 x 4096 bf16: forward 0.140 ms for 0.54 GB (59 % of the measured
+// copy rate), gradients 0.306 ms for 0.94 GB (47 %).  Neither HBM nor a pipe is full
+// (special functions 55 %, issue 50 %): a round is a chain of ~2 us (gates, block barrier,
+// exchange, apply) and 128 (sequence, channel group) pairs give each SM only about two CTAs to
+// overlap, unevenly (256 CTAs on 148 SMs).  With 16 sequences of 1024 tokens, the same bytes, no
+// exchange and four CTAs per SM, the forward takes 0.108 ms (76 %).  Deeper prefetch (3 or 4
+// stages), 32-channel CTAs and computing the next round's gates before the exchange is awaited
+// changed the first case by less than 5 %.
 #include <cmath>
 #include <type_traits>
 
@@ -32,10 +39,7 @@ constexpr int kMaxSplit = 16;       // CTAs of a cluster
 // Warps of a CTA, and the consecutive tokens (run) of each.  Long runs share the cost of
 // a round's exchange; the gradients keep three times as much per token in registers.
 constexpr int kFwdWarps = 4, kFwdRun = kTile / kFwdWarps;
-#ifndef FST
-#define FST 2
-#endif
-constexpr int kFwdStages = FST;
+constexpr int kFwdStages = 2;
 constexpr int kBwdWarps = 8, kBwdRun = kTile / kBwdWarps;
 
 // How a lane's two channels lie and how rows reach shared memory.
@@ -358,8 +362,8 @@ __host__ __device__ constexpr size_t exchange_bytes(int split) {
 
 __device__ __forceinline__ void st_async_f32x4(uint32_t remote, float4 v, uint32_t remote_bar) {
   asm volatile(
-      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
-          remote),
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 "
+      "[%0], {%1, %2, %3, %4}, [%5];" ::"r"(remote),
       "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(remote_bar)
       : "memory");
 }
@@ -758,8 +762,10 @@ __global__ void __launch_bounds__(kDirectThreads)
 glr_fwd_direct_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ state_out,
                       Th* __restrict__ h, float* __restrict__ chunk_states) {
   const int D = p.D;
-  const int seq = static_cast<int>(blockIdx.x / p.groups), c0 = static_cast<int>(blockIdx.x % p.groups) * kDirectChan;
-  const int cA = c0 + (PAIR ? 2 : 1) * static_cast<int>(threadIdx.x), cB = cA + (PAIR ? 1 : kDirectThreads);
+  const int seq = static_cast<int>(blockIdx.x / p.groups);
+  const int c0 = static_cast<int>(blockIdx.x % p.groups) * kDirectChan;
+  const int cA = c0 + (PAIR ? 2 : 1) * static_cast<int>(threadIdx.x);
+  const int cB = cA + (PAIR ? 1 : kDirectThreads);
   const bool okA = cA < D, okB = cB < D;
   if (c0 == 0 && threadIdx.x == 0) check_offsets(p.L, seq, p.err);
   if (!okA) return;
@@ -803,8 +809,10 @@ glr_bwd_direct_kernel(Args p, const float* __restrict__ chunk_states, const Tu* 
                       Tg* __restrict__ dr, Tg* __restrict__ di, float* __restrict__ d_state_in,
                       float* __restrict__ partial) {
   const int D = p.D;
-  const int seq = static_cast<int>(blockIdx.x / p.groups), c0 = static_cast<int>(blockIdx.x % p.groups) * kDirectChan;
-  const int cA = c0 + (PAIR ? 2 : 1) * static_cast<int>(threadIdx.x), cB = cA + (PAIR ? 1 : kDirectThreads);
+  const int seq = static_cast<int>(blockIdx.x / p.groups);
+  const int c0 = static_cast<int>(blockIdx.x % p.groups) * kDirectChan;
+  const int cA = c0 + (PAIR ? 2 : 1) * static_cast<int>(threadIdx.x);
+  const int cB = cA + (PAIR ? 1 : kDirectThreads);
   const bool okA = cA < D, okB = cB < D;
   if (c0 == 0 && threadIdx.x == 0) check_offsets(p.L, seq, p.err);
   if (!okA) return;
@@ -963,9 +971,9 @@ int split_of(const SeqLayout& L, int D) {
 }
 
 // Whether threads walk their sequences alone: up to 32 tokens per sequence (16 on average where the
-// lengths differ, which the host does not know).  Measured in us, forward / gradients, alone and by
-// tiles: 256 x 4 x 4096 bf16 15 / 32 and 130 / 253, 32 x 16 x 2048 6.0 / 9.6 and 10.9 / 20.9, 128 x 64 x
-// 4096 77 / 196 and 74 / 169.
+// lengths differ, which the host does not know).  Measured in us, forward / gradients, alone
+// and by tiles: 256 x 4 x 4096 bf16 15 / 32 and 130 / 253, 32 x 16 x 2048 6.0 / 9.6 and 10.9 / 20.9,
+// 128 x 64 x 4096 77 / 196 and 74 / 169.
 bool direct(const SeqLayout& L) {
   return L.Ttot <= (L.T > 0 ? 32ll : 16ll) * L.nseq;
 }
@@ -1021,17 +1029,20 @@ cudaError_t launch_glr_fwd(const void* x, const void* r, const void* i, DType in
       if (alone) {
         using Ti = decltype(ti);
         using Th = decltype(th);
-        auto kern = D % 2 == 0 ? glr_fwd_direct_kernel<Ti, Th, true> : glr_fwd_direct_kernel<Ti, Th, false>;
-        kern<<<static_cast<unsigned>(blocks), kDirectThreads, 0, s>>>(p, state_in, state_out,
-                                                                       static_cast<Th*>(h), chunk_states);
+        auto kern = D % 2 == 0 ? glr_fwd_direct_kernel<Ti, Th, true>
+                               : glr_fwd_direct_kernel<Ti, Th, false>;
+        kern<<<static_cast<unsigned>(blocks), kDirectThreads, 0, s>>>(
+            p, state_in, state_out, static_cast<Th*>(h), chunk_states);
         return cudaGetLastError();
       }
       return by_mode(in_t, D, [&](auto mode) {
         using Ti = decltype(ti);
         using Th = decltype(th);
         constexpr int M = decltype(mode)::value;
-        const size_t smem = exchange_bytes(p.split) + kFwdStages * 3 * kFwdWarps * run_bytes<Ti, M, kFwdRun>();
-        return launch_split(glr_fwd_kernel<Ti, Th, M>, kFwdWarps * 32, smem, blocks, p.split, s, p, state_in,
+        const size_t smem = exchange_bytes(p.split) +
+                            kFwdStages * 3 * kFwdWarps * run_bytes<Ti, M, kFwdRun>();
+        return launch_split(glr_fwd_kernel<Ti, Th, M>, kFwdWarps * 32, smem, blocks, p.split, s,
+                            p, state_in,
                             state_out, static_cast<Th*>(h), chunk_states);
       });
     });
@@ -1060,7 +1071,8 @@ cudaError_t launch_glr_bwd(const void* x, const void* r, const void* i, DType in
           using Ti = decltype(ti);
           using Tu = decltype(tu);
           using Tg = decltype(tg);
-          auto kern = D % 2 == 0 ? glr_bwd_direct_kernel<Ti, Tu, Tg, true> : glr_bwd_direct_kernel<Ti, Tu, Tg, false>;
+          auto kern = D % 2 == 0 ? glr_bwd_direct_kernel<Ti, Tu, Tg, true>
+                                 : glr_bwd_direct_kernel<Ti, Tu, Tg, false>;
           kern<<<static_cast<unsigned>(blocks), kDirectThreads, 0, s>>>(
               p, chunk_states, static_cast<const Tu*>(d_h), d_state_out, static_cast<Tg*>(dx),
               static_cast<Tg*>(dr), static_cast<Tg*>(di), d_state_in, partial);
@@ -1074,7 +1086,8 @@ cudaError_t launch_glr_bwd(const void* x, const void* r, const void* i, DType in
           const size_t smem =
               exchange_bytes(p.split) + 2 * kBwdWarps * 32 * sizeof(F2) +
               2 * kBwdWarps * (3 * run_bytes<Ti, M, kBwdRun>() + run_bytes<Tu, M, kBwdRun>());
-          return launch_split(glr_bwd_kernel<Ti, Tu, Tg, M>, kBwdWarps * 32, smem, blocks, p.split, s, p,
+          return launch_split(glr_bwd_kernel<Ti, Tu, Tg, M>, kBwdWarps * 32, smem, blocks,
+                              p.split, s, p,
                               chunk_states, static_cast<const Tu*>(d_h), d_state_out,
                               static_cast<Tg*>(dx), static_cast<Tg*>(dr), static_cast<Tg*>(di),
                               d_state_in, partial);

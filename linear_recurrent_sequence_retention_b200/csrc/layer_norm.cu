@@ -1,6 +1,8 @@
 // Layer norm over the last dimension and its gradients (formulas in
 // include/retention.h).  HBM-bound: the forward reads x and writes y once, the
-// gradients read x and d_y and write dx once.
+// gradients read x and d_y and write dx once.  Measured at 16384 x 4096 bf16: forward
+// 0.047 ms (5.7 TB/s, 87 % of the measured copy rate), gradients 0.077 ms (5.2 TB/s, 80 %), of
+// which 4.5 us are the sum of the weights' partial gradients.
 //
 // Forward: a row belongs to one warp (up to 1024 channels) or one block and stays in
 // registers between its two statistics passes and the output.
@@ -84,8 +86,9 @@ ln_fwd_kernel(const Tx* __restrict__ x, const float* __restrict__ w, const float
 // Any width: one channel at a time.
 template <typename Tx, int TPR, int NV>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
-ln_fwd_any_kernel(const Tx* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, float eps,
-                  float invD, AnyOut y, float* __restrict__ mean, float* __restrict__ rstd, int ntok, int D) {
+ln_fwd_any_kernel(const Tx* __restrict__ x, const float* __restrict__ w,
+                  const float* __restrict__ b, float eps, float invD, AnyOut y,
+                  float* __restrict__ mean, float* __restrict__ rstd, int ntok, int D) {
   constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
   __shared__ float part[2 * (TPR / 32)];
   const int t = threadIdx.x % TPR;
@@ -287,7 +290,8 @@ ln_bwd_kernel(const Tx* __restrict__ x, const Tu* __restrict__ dy, const float* 
 // Any width: one channel at a time.
 template <typename Tx, typename Tu, int TPR, int NV>
 __global__ void __launch_bounds__(bwd_threads(TPR))
-ln_bwd_any_kernel(const Tx* __restrict__ x, const Tu* __restrict__ dy, const float* __restrict__ mean, const float* __restrict__ rstd,
+ln_bwd_any_kernel(const Tx* __restrict__ x, const Tu* __restrict__ dy,
+                  const float* __restrict__ mean, const float* __restrict__ rstd,
                   const float* __restrict__ w, AnyOut dx, float* __restrict__ partial, int ntok,
                   int D) {
   constexpr int kThreads = bwd_threads(TPR), kGroups = kThreads / TPR;
@@ -373,6 +377,7 @@ Shape fwd_shape(int ntok, int D) {
     if (D <= 512) return {true, 32, 16};
     if (few && D <= 4096) return D <= 1024 ? Shape{true, 128, 8} : Shape{true, 512, 8};
     if (D <= 1024) return {true, 32, 32};
+    if (D <= 2048) return {true, 128, 16};
     if (D <= 4096) return {true, 128, 32};
     if (D <= 8192) return {true, 256, 32};
     return {true, 512, 32};
@@ -386,6 +391,7 @@ Shape fwd_shape(int ntok, int D) {
 // block cannot be larger, and their weights are read again for every row.
 Shape bwd_shape(int D) {
   if (D % 8 == 0) {
+    if (D <= 256) return {true, 32, 8};
     int tpr = 32;
     while (tpr < 512 && tpr * 16 < D) tpr *= 2;
     return {true, tpr, tpr * 16 < D ? 32 : 16};
@@ -419,10 +425,11 @@ cudaError_t with_shape(const Shape& s, F&& f) {
 }
 // Compiles only what a shape table can name.
 constexpr bool fwd_vec(int tpr, int ch) {
-  return tpr == 32 || (tpr == 128 && ch != 16) || (tpr == 256 && ch == 32) ||
-         (tpr == 512 && ch != 16);
+  return tpr == 32 || tpr == 128 || (tpr == 256 && ch == 32) || (tpr == 512 && ch != 16);
 }
-constexpr bool bwd_vec(int tpr, int ch) { return ch == 16 || (tpr == 512 && ch == 32); }
+constexpr bool bwd_vec(int tpr, int ch) {
+  return ch == 16 || (tpr == 32 && ch == 8) || (tpr == 512 && ch == 32);
+}
 constexpr bool any_width(int tpr, int ch) {
   return (tpr == 32 && ch == 8) || (tpr == 128 && ch == 8) || (tpr == 256 && ch == 16) ||
          (tpr == 512 && ch == 32);
