@@ -55,6 +55,8 @@
  *             of the same call may have run.  RET_ERR_UNSUPPORTED means the
  *             arguments are valid but the library has no kernel for the
  *             shape or dtype combination; there is no fallback path.
+ *   Workspaces: calls (or captured graphs) that use one workspace must not run
+ *             at the same time; separate workspaces make them independent.
  *   Aliasing: outputs must not overlap inputs, except that
  *             retention_recurrent_step(s) update `state` in place by design,
  *             retention_rope may rotate q and k in place and
@@ -518,7 +520,7 @@ RET_API ret_status msr_norm_gate(const void* o, ret_dtype o_dtype, const ret_nor
  * it is stored as bf16.  1 - a^2 is formed without cancellation for decays near
  * one.  No workspace.  Inconsistent cu_seqlens are clamped and reported as
  * RET_ERR_DEVICE_DATA.
- * Supported: any T (packed T = 0 included) with B*T < 2^31, D in 1..2^20;
+ * Supported: any T (packed T = 0 included) with B*T + 2048 < 2^31, D in 1..2^20;
  * element offsets are 64-bit.
  */
 #define RETENTION_GLR_CHUNK 64

@@ -748,7 +748,8 @@ ret_status glr_layout(int B, int T, int D, const int32_t* cu, int nseq, ret::Seq
   if (nseq < 0 || D < 1) return RET_ERR_INVALID_ARG;
   if (nseq > 0 ? (B != 1 || T < 0) : (B < 1 || T < 1)) return RET_ERR_INVALID_ARG;
   const long long Ttot = nseq > 0 ? T : static_cast<long long>(B) * T;
-  if (!fits_int(Ttot + ret::kGlrChunk)) return RET_ERR_INVALID_ARG;
+  // the kernels form token indexes up to one round (16 tiles) past the end
+  if (!fits_int(Ttot + 32 * ret::kGlrChunk)) return RET_ERR_INVALID_ARG;
   if (D > kMaxGlrChannels) return RET_ERR_UNSUPPORTED;
   L->cu = cu;
   L->nseq = nseq > 0 ? nseq : B;

@@ -20,6 +20,8 @@ def test_glr_sizes():
     assert ops.glr_chunk_slots(1, 0, nseq=3) == 3
     assert ops.glr_chunk_slots(0, 10) == 0 and ops.glr_chunk_slots(2, 10, nseq=3) == 0
     assert ops.glr_chunk_slots(1 << 16, 1 << 15) == 0            # 2^31 tokens
+    assert ops.glr_chunk_slots(1, (1 << 31) - 2048) == 0          # indexes past the last round
+    assert ops.glr_chunk_slots(1, (1 << 31) - 2049) > 0
     need = ops.glr_bwd_workspace_size(2, 8192, 4096)
     assert need > 0 and need % 256 == 0
     assert ops.glr_bwd_workspace_size(2, 8192, 0) == 0
