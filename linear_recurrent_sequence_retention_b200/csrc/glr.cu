@@ -928,9 +928,10 @@ template <typename F>
 cudaError_t by_type(DType t, F&& f) {
   return t == DType::F32 ? f(float{}) : f(__nv_bfloat16{});
 }
+// The rows of every staged tensor have to allow the pieces: those of the narrowest type decide.
 template <typename F>
-cudaError_t by_mode(DType in_t, int D, F&& f) {
-  const int e = in_t == DType::F32 ? 4 : 2;
+cudaError_t by_mode(bool any_bf16, int D, F&& f) {
+  const int e = any_bf16 ? 2 : 4;
   if (D * static_cast<long long>(e) % 16 == 0) return f(std::integral_constant<int, kWide>{});
   if (D % 2 == 0) return f(std::integral_constant<int, kEven>{});
   return f(std::integral_constant<int, kOdd>{});
@@ -1035,7 +1036,7 @@ cudaError_t launch_glr_fwd(const void* x, const void* r, const void* i, DType in
             p, state_in, state_out, static_cast<Th*>(h), chunk_states);
         return cudaGetLastError();
       }
-      return by_mode(in_t, D, [&](auto mode) {
+      return by_mode(in_t == DType::BF16, D, [&](auto mode) {
         using Ti = decltype(ti);
         using Th = decltype(th);
         constexpr int M = decltype(mode)::value;
@@ -1078,7 +1079,7 @@ cudaError_t launch_glr_bwd(const void* x, const void* r, const void* i, DType in
               static_cast<Tg*>(dr), static_cast<Tg*>(di), d_state_in, partial);
           return cudaGetLastError();
         }
-        return by_mode(in_t, D, [&](auto mode) {
+        return by_mode(in_t == DType::BF16 || dh_t == DType::BF16, D, [&](auto mode) {
           using Ti = decltype(ti);
           using Tu = decltype(tu);
           using Tg = decltype(tg);

@@ -141,6 +141,27 @@ def test_forward_and_gradients(dtype, out, B, T, D, state):
     ops.check_device_error()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("up", ["f32", "bf16"])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [4, 20, 33, 66, 100, 136])
+def test_gradients_of_mixed_types(dtype, up, out, D):
+    """Each type of the inputs, of d_h and of the gradients with rows that divide by 16 bytes in
+    one type and not in the other (4, 20, 100), in both, and in neither."""
+    B, T = 2, 150
+    x, r, i, lam, dh, S0, dS = make(B, T, D, dtype, seed=D)
+    dh = dh.to(W.torch_dtype(up))
+    ref = Reference(x, r, i, lam, dh, S0, dS)
+    xd, rd, id_, ld, dhd, S0d, dSd = cuda(x, r, i, lam, dh, S0, dS)
+    h, S, chunks = ops.glr_fwd(xd, rd, id_, ld, state_in=S0d, return_state=True,
+                               return_chunks=True, out_dtype=W.torch_dtype(out))
+    ref.check_forward(h, S, T, chunks)
+    got = ops.glr_bwd(xd, rd, id_, ld, chunks, dhd, d_state_out=dSd, return_d_state=True,
+                      grad_dtype=W.torch_dtype(out))
+    ref.check_gradients(got, T)
+    ops.check_device_error()
+
+
 PACKED = [[0, 1, 64, 65, 0, 300, 127], [5], [0, 0], [1] * 40, [3, 0, 0, 2, 1, 0] * 30, [700, 1, 1200]]
 
 
