@@ -39,14 +39,19 @@ constexpr int kMaxSplit = 16;       // CTAs of a cluster
 // Warps of a CTA, and the consecutive tokens (run) of each.  Long runs share the cost of
 // a round's exchange; the gradients keep three times as much per token in registers.
 constexpr int kFwdWarps = 4, kFwdRun = kTile / kFwdWarps;
-constexpr int kFwdStages = 2;
 constexpr int kBwdWarps = 8, kBwdRun = kTile / kBwdWarps;
+// Rounds whose rows are in shared memory at once.  Two of float32 would leave room for only one
+// CTA of the gradients on an SM (0.320 ms instead of 0.197 ms at 2 x 8192 x 2048), and two of the
+// forward (0.062 instead of 0.056 ms at 17 sequences, 9001 tokens x 1001; even at 2 x 8192 x 2048).
+// With one the next rows are on their way from the moment these have been read.
+template <typename T> constexpr int stages() { return sizeof(T) == 2 ? 2 : 1; }
 
 // How a lane's two channels lie and how rows reach shared memory.
-//   kWide: channels 2l, 2l+1; rows are copied in 16-byte pieces (D e bytes divide by 16)
-//   kEven: channels 2l, 2l+1; 4-byte pieces (D even)
-//   kOdd:  channels l, l+32; 4-byte pieces; a bf16 row may start in the middle of one and
-//          then takes 33 of them
+//   kWide: channels 2l, 2l+1; rows start on 16-byte boundaries (D e bytes divide by 16)
+//   kEven: channels 2l, 2l+1 (D even)
+//   kOdd:  channels l, l+32
+// All rows are copied in 16-byte pieces; those of kEven and kOdd may start inside their first one
+// and have one piece more.
 enum { kWide = 0, kEven = 1, kOdd = 2 };
 
 // ---- pairs of floats (one instruction for both) ------------------------------
@@ -156,11 +161,10 @@ struct Args {
   unsigned* err;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+// Copies `bytes` and fills the rest of the 16 with zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -170,102 +174,86 @@ __device__ __forceinline__ void cp_wait() {
 
 // Bytes of a staged row, and of a warp's rows of one array.
 template <typename T, int MODE> constexpr int row_bytes() {
-  return kChan * static_cast<int>(sizeof(T)) + (MODE == kOdd && sizeof(T) == 2 ? 4 : 0);
+  return kChan * static_cast<int>(sizeof(T)) + (MODE == kWide ? 0 : 16);
 }
 template <typename T, int MODE, int RUN> constexpr int run_bytes() {
-  return (RUN * row_bytes<T, MODE>() + 15) / 16 * 16;
+  return RUN * row_bytes<T, MODE>();
+}
+// Elements by which row t lies inside its first piece (c0 is a multiple of a piece).
+template <typename T, int MODE> __device__ __forceinline__ int row_shift(int t, int D) {
+  if constexpr (MODE == kWide) return 0;
+  return static_cast<int>(static_cast<unsigned>(t) * static_cast<unsigned>(D) &
+                          (16 / sizeof(T) - 1));
 }
 
-// Copies a warp's rows t .. t+7, channels c0 .. c0+63, to `dst`; rows at or past
-// t1 are filled with `fill` (two bf16, or the float) instead: r = -inf, and zeros
-// elsewhere, make a token the identity.  `total` is the tensor's element count.
-template <typename T, int MODE, int RUN>
-__device__ __forceinline__ void stage_rows(char* dst, const T* src, int t, int t1, int c0, int D,
-                                           size_t total, uint32_t fill, int lane) {
-  constexpr int kPiece = MODE == kWide ? 16 : 4;
-  constexpr int kRow = row_bytes<T, MODE>();
-  constexpr int kPer = kRow / kPiece;                     // pieces of a row
-  constexpr int kElems = kPiece / static_cast<int>(sizeof(T));
-  const uint32_t d = tc::smem_u32(dst);
-#pragma unroll
-  for (int k = 0; k < (RUN * kPer + 31) / 32; ++k) {
-    const int idx = k * 32 + lane, row = idx / kPer, p = idx % kPer;
-    if (RUN * kPer % 32 != 0 && row >= RUN) break;
-    const uint32_t to = d + row * kRow + p * kPiece;
+// Copies a warp's rows t .. t+RUN-1, channels c0 .. c0+63, of N arrays of one shape to `dst`, one
+// run_bytes after the other; rows at or past t1 are filled with `fill` (two bf16, or the float)
+// instead: r = -inf, and zeros elsewhere, make a token the identity.  `total` is the tensor's
+// element count: nothing past it is read.  (4-byte pieces, which fit every row, took 0.147 ms
+// instead of 0.052 ms forward and 0.182 instead of 0.098 ms backward at 8192 x 1001 bf16.)
+template <typename T, int MODE, int RUN, int N>
+__device__ __forceinline__ void stage_rows(char* dst, const T* const (&src)[N],
+                                           const uint32_t (&fill)[N], int t, int t1, int c0, int D,
+                                           size_t total, int lane) {
+  constexpr int kElems = 16 / static_cast<int>(sizeof(T));
+  constexpr int kPer = kChan / kElems;                    // pieces of a row, without the last
+  constexpr int kStep = 32 / kPer;                        // rows per access of the warp
+  constexpr int kArray = run_bytes<T, MODE, RUN>();
+  const int width = min(kChan, D - c0);
+  const auto piece = [&](int row, int q) {
+    char* to = dst + row * row_bytes<T, MODE>() + q * 16;
     if (t + row >= t1) {
-      uint32_t* q = reinterpret_cast<uint32_t*>(dst + row * kRow + p * kPiece);
 #pragma unroll
-      for (int n = 0; n < kPiece / 4; ++n) q[n] = fill;
-      continue;
+      for (int n = 0; n < N; ++n)
+        *reinterpret_cast<uint4*>(to + n * kArray) =
+            make_uint4(fill[n], fill[n], fill[n], fill[n]);
+      return;
     }
     const size_t at = static_cast<size_t>(t + row) * D + c0;
-    if constexpr (MODE == kOdd && sizeof(T) == 2) {
-      const size_t from = (at & ~static_cast<size_t>(1)) + 2 * p;     // even: 4-byte aligned
-      if (from >= at + min(kChan, D - c0)) continue;
-      if (from + 1 < total)
-        cp_async4(to, src + from);
-      else                                                // the tensor's last element
-        *reinterpret_cast<T*>(dst + row * kRow + p * kPiece) = src[from];
-    } else {
-      if (c0 + p * kElems >= D) continue;
-      if constexpr (kPiece == 16)
-        cp_async16(to, src + at + p * kElems);
-      else
-        cp_async4(to, src + at + p * kElems);
-    }
+    const int in = q * kElems - row_shift<T, MODE>(t + row, D);      // first channel of the piece
+    if (in >= width) return;
+    const size_t from = at + in;
+    const int bytes =
+        MODE == kWide ? 16
+                      : static_cast<int>(min(static_cast<size_t>(kElems), total - from)) *
+                            static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      cp_async16(tc::smem_u32(to + n * kArray), src[n] + from, bytes);
+  };
+#pragma unroll
+  for (int k = 0; k < RUN / kStep; ++k) piece(k * kStep + lane / kPer, lane % kPer);
+  if constexpr (MODE != kWide) {
+    static_assert(RUN <= 32, "one last piece per lane");
+    if (lane < RUN) piece(lane, kPer);
   }
 }
 
-// The same for a run that lies whole inside the sequence: `from` is the lane's first piece
+// kWide, a run that lies whole inside the sequence: `from` is the lane's first piece
 // (stage_from), the copies differ by whole rows only.
-template <typename T, int MODE>
+template <typename T>
 __device__ __forceinline__ const T* stage_from(const T* src, int t, int c0, int D, int lane) {
-  constexpr int kPer = row_bytes<T, MODE>() / (MODE == kWide ? 16 : 4);
-  constexpr int kElems = (MODE == kWide ? 16 : 4) / static_cast<int>(sizeof(T));
-  const int row = kPer < 32 ? lane / kPer : 0, p = kPer < 32 ? lane % kPer : lane;
-  return src + static_cast<ptrdiff_t>(t + row) * D + c0 + p * kElems;
+  constexpr int kElems = 16 / static_cast<int>(sizeof(T)), kPer = kChan / kElems;
+  return src + static_cast<ptrdiff_t>(t + lane / kPer) * D + c0 + lane % kPer * kElems;
 }
-template <typename T, int MODE, int RUN>
+template <typename T, int RUN>
 __device__ __forceinline__ void stage_full(char* dst, const T* from, int c0, int D, int lane) {
-  constexpr int kPiece = MODE == kWide ? 16 : 4;
-  constexpr int kPer = row_bytes<T, MODE>() / kPiece;
-  constexpr int kElems = kPiece / static_cast<int>(sizeof(T));
-  const uint32_t d = tc::smem_u32(dst) + lane * kPiece;
-  if constexpr (kPer <= 32) {
-    constexpr int kStep = 32 / kPer;                      // rows per copy of the warp
-    if (c0 + (lane % kPer) * kElems >= D) return;
+  constexpr int kElems = 16 / static_cast<int>(sizeof(T)), kPer = kChan / kElems;
+  constexpr int kStep = 32 / kPer;
+  if (c0 + lane % kPer * kElems >= D) return;
+  const uint32_t d = tc::smem_u32(dst) + lane * 16;
 #pragma unroll
-    for (int k = 0; k < RUN / kStep; ++k) {
-      if constexpr (kPiece == 16)
-        cp_async16(d + k * 32 * kPiece, from + static_cast<ptrdiff_t>(k * kStep) * D);
-      else
-        cp_async4(d + k * 32 * kPiece, from + static_cast<ptrdiff_t>(k * kStep) * D);
-    }
-  } else {                                                // float32 in 4-byte pieces: two per row
-    const bool okA = c0 + lane < D, okB = c0 + 32 + lane < D;
-#pragma unroll
-    for (int k = 0; k < RUN; ++k) {
-      if (okA) cp_async4(d + k * 256, from + static_cast<ptrdiff_t>(k) * D);
-      if (okB) cp_async4(d + k * 256 + 128, from + static_cast<ptrdiff_t>(k) * D + 32);
-    }
-  }
-}
-// One warp's rows of one array, by whichever way fits.
-template <typename T, int MODE, int RUN>
-__device__ __forceinline__ void stage(char* dst, const T* src, const T* from, int t, int t1, int c0,
-                                      int D, size_t total, uint32_t fill, int lane) {
-  if ((MODE != kOdd || sizeof(T) == 4) && t + RUN <= t1)
-    stage_full<T, MODE, RUN>(dst, from, c0, D, lane);
-  else
-    stage_rows<T, MODE, RUN>(dst, src, t, t1, c0, D, total, fill, lane);
+  for (int k = 0; k < RUN / kStep; ++k)
+    cp_async16(d + k * 512, from + static_cast<ptrdiff_t>(k * kStep) * D, 16);
 }
 
 // A lane's two channels of staged row k, token t.
 template <typename T, int MODE>
-__device__ __forceinline__ F2 row_pair(const char* st, int k, int t, int c0, int D, int lane) {
-  const char* row = st + k * row_bytes<T, MODE>();
+__device__ __forceinline__ F2 row_pair(const char* st, int k, int t, int D, int lane) {
+  const char* row = st + k * row_bytes<T, MODE>() +
+                    row_shift<T, MODE>(t, D) * static_cast<int>(sizeof(T));
   if constexpr (MODE == kOdd && sizeof(T) == 2) {
-    const unsigned short* q = reinterpret_cast<const unsigned short*>(row) + ((t & D & 1) ^ (c0 & 1));
+    const unsigned short* q = reinterpret_cast<const unsigned short*>(row);
     return make_float2(__uint_as_float(static_cast<uint32_t>(q[lane]) << 16),
                        __uint_as_float(static_cast<uint32_t>(q[lane + 32]) << 16));
   } else if constexpr (sizeof(T) == 2) {
@@ -351,13 +339,12 @@ __device__ __forceinline__ float4 pack(const Map& m) {
 // next map only after that, so a map received tells that the sender's warps have
 // read everything of the round before last.
 struct Exchange {
-  Maps warp[2][8];
   uint64_t bar[2];
   int abort;
   int pad[3];
 };
-__host__ __device__ constexpr size_t exchange_bytes(int split) {
-  return sizeof(Exchange) + (split > 1 ? 2 * split * sizeof(Maps) : 0);
+__host__ __device__ constexpr size_t exchange_bytes(int split, int warps) {
+  return sizeof(Exchange) + 2 * (warps + (split > 1 ? split : 0)) * sizeof(Maps);
 }
 
 __device__ __forceinline__ void st_async_f32x4(uint32_t remote, float4 v, uint32_t remote_bar) {
@@ -414,12 +401,13 @@ glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ s
                Th* __restrict__ h, float* __restrict__ chunk_states) {
   extern __shared__ __align__(16) char smem[];
   constexpr int kWarps = kFwdWarps, kRun = kFwdRun;
-  constexpr int kArray = run_bytes<Ti, MODE, kRun>();
+  constexpr int kArray = run_bytes<Ti, MODE, kRun>(), kStages = stages<Ti>();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int S = p.split, rank = static_cast<int>(blockIdx.x % S);
   Exchange& ex = *reinterpret_cast<Exchange*>(smem);
-  Maps* cta_maps = reinterpret_cast<Maps*>(smem + sizeof(Exchange));      // [2][S]
-  char* ring = smem + exchange_bytes(S) + warp * (kFwdStages * 3 * kArray);
+  Maps(*warp_maps)[kWarps] = reinterpret_cast<Maps(*)[kWarps]>(smem + sizeof(Exchange));   // [2]
+  Maps* cta_maps = reinterpret_cast<Maps*>(warp_maps + 2);                // [2][S]
+  char* ring = smem + exchange_bytes(S, kWarps) + warp * (kStages * 3 * kArray);
   const int pair = static_cast<int>(blockIdx.x / S);
   const int seq = pair / p.groups, c0 = (pair % p.groups) * kChan;
   const int D = p.D;
@@ -436,52 +424,53 @@ glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ s
   const uint32_t minus_inf = sizeof(Ti) == 2 ? 0xff80ff80u : 0xff800000u;
   const auto first = [&](int j) { return t0 + ((j * S + rank) * kWarps + warp) * kRun; };
   const ptrdiff_t stride = static_cast<ptrdiff_t>(S) * kTile * D;          // of a round
-  const Ti* xp = stage_from<Ti, MODE>(x, first(0), c0, D, lane);
-  const Ti* rp = stage_from<Ti, MODE>(r, first(0), c0, D, lane);
-  const Ti* ip = stage_from<Ti, MODE>(i, first(0), c0, D, lane);
-  int fill = 0;                         // stage of the next fetch
+  const Ti* const src[3] = {x, r, i};
+  const uint32_t pad[3] = {0u, minus_inf, 0u};
+  const Ti* from[3];                    // of the next fetch
+#pragma unroll
+  for (int n = 0; n < 3; ++n) from[n] = stage_from(src[n], first(0), c0, D, lane);
   const auto fetch = [&](int j) {
-    char* st = ring + fill * 3 * kArray;
-    fill = fill + 1 == kFwdStages ? 0 : fill + 1;
     if (j < rounds) {
+      char* st = ring + j % kStages * 3 * kArray;
       const int t = first(j);
-      stage<Ti, MODE, kRun>(st, x, xp, t, t1, c0, D, total, 0, lane);
-      stage<Ti, MODE, kRun>(st + kArray, r, rp, t, t1, c0, D, total, minus_inf, lane);
-      stage<Ti, MODE, kRun>(st + 2 * kArray, i, ip, t, t1, c0, D, total, 0, lane);
-      xp += stride;
-      rp += stride;
-      ip += stride;
+      if (MODE == kWide && t + kRun <= t1) {
+#pragma unroll
+        for (int n = 0; n < 3; ++n) stage_full<Ti, kRun>(st + n * kArray, from[n], c0, D, lane);
+      } else {
+        stage_rows<Ti, MODE, kRun>(st, src, pad, t, t1, c0, D, total, lane);
+      }
+#pragma unroll
+      for (int n = 0; n < 3; ++n) from[n] += stride;
     }
     cp_commit();
   };
-#pragma unroll
-  for (int j = 0; j < kFwdStages - 1; ++j) fetch(j);
+  fetch(0);
   const F2 lm = load2(p.lam, 0, cA, cB, D);
   const F2 ysc = make_float2(p.c * softplus(lm.x), p.c * softplus(lm.y));
   F2 carry = load2(state_in, static_cast<size_t>(seq) * D, cA, cB, D);
   exchange_begin(ex, S);
   const auto run = [&](auto small) {
-    int use = 0;
     for (int j = 0; j < rounds; ++j) {
-      fetch(j + kFwdStages - 1);
-      cp_wait<kFwdStages - 1>();
+      if (kStages > 1) fetch(j + 1);
+      cp_wait<kStages - 1>();
       __syncwarp();
-      const char* st = ring + use * 3 * kArray;
-      use = use + 1 == kFwdStages ? 0 : use + 1;
+      const char* st = ring + j % kStages * 3 * kArray;
       const int t = first(j);
       F2 a[kRun], v[kRun];
       Map m = identity();
 #pragma unroll
       for (int k = 0; k < kRun; ++k) {
-        const F2 xv = row_pair<Ti, MODE>(st, k, t + k, c0, D, lane);
-        const F2 rv = row_pair<Ti, MODE>(st + kArray, k, t + k, c0, D, lane);
-        const F2 iv = row_pair<Ti, MODE>(st + 2 * kArray, k, t + k, c0, D, lane);
+        const F2 xv = row_pair<Ti, MODE>(st, k, t + k, D, lane);
+        const F2 rv = row_pair<Ti, MODE>(st + kArray, k, t + k, D, lane);
+        const F2 iv = row_pair<Ti, MODE>(st + 2 * kArray, k, t + k, D, lane);
         F2 root;
         decay<decltype(small)::value>(mul(ysc, sigmoid(rv)), a[k], root);
         v[k] = mul(mul(root, sigmoid(iv)), xv);
         m = k == 0 ? Map{a[0], v[0]} : then(m, Map{a[k], v[k]});
       }
-      Maps* wm = ex.warp[j & 1];
+      __syncwarp();                       // the buffer refilled next was read to here
+      if (kStages == 1) fetch(j + 1);
+      Maps* wm = warp_maps[j & 1];
       wm[warp][lane] = pack(m);
       __syncthreads();
       F2 enter, hs;                       // the states that enter the tile and the warp's run
@@ -560,13 +549,14 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
   extern __shared__ __align__(16) char smem[];
   constexpr int kWarps = kBwdWarps, kRun = kBwdRun;
   constexpr int kArray = run_bytes<Ti, MODE, kRun>(), kUp = run_bytes<Tu, MODE, kRun>();
-  constexpr int kStage = 3 * kArray + kUp;
+  constexpr int kStage = 3 * kArray + kUp, kStages = stages<Ti>();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int S = p.split, rank = static_cast<int>(blockIdx.x % S);
   Exchange& ex = *reinterpret_cast<Exchange*>(smem);
-  Maps* cta_maps = reinterpret_cast<Maps*>(smem + sizeof(Exchange));      // [2][S]
-  F2(*wf)[kWarps][32] = reinterpret_cast<F2(*)[kWarps][32]>(smem + exchange_bytes(S));
-  char* ring = reinterpret_cast<char*>(wf + 2) + warp * (2 * kStage);
+  Maps(*warp_maps)[kWarps] = reinterpret_cast<Maps(*)[kWarps]>(smem + sizeof(Exchange));   // [2]
+  Maps* cta_maps = reinterpret_cast<Maps*>(warp_maps + 2);                // [2][S]
+  F2(*wf)[kWarps][32] = reinterpret_cast<F2(*)[kWarps][32]>(smem + exchange_bytes(S, kWarps));
+  char* ring = reinterpret_cast<char*>(wf + 2) + warp * (kStages * kStage);
   const int pair = static_cast<int>(blockIdx.x / S);
   const int seq = pair / p.groups, c0 = (pair % p.groups) * kChan;
   const int D = p.D;
@@ -582,24 +572,15 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
   const int rounds = ceil_div(t1 - t0, kTile * S);
   const uint32_t minus_inf = sizeof(Ti) == 2 ? 0xff80ff80u : 0xff800000u;
   const auto first = [&](int j) { return t0 + ((j * S + rank) * kWarps + warp) * kRun; };
-  const ptrdiff_t stride = static_cast<ptrdiff_t>(S) * kTile * D;          // of a round
-  const int last = first(rounds - 1);
-  const Ti* xp = stage_from<Ti, MODE>(x, last, c0, D, lane);
-  const Ti* rp = stage_from<Ti, MODE>(r, last, c0, D, lane);
-  const Ti* ip = stage_from<Ti, MODE>(i, last, c0, D, lane);
-  const Tu* up = stage_from<Tu, MODE>(dh, last, c0, D, lane);
+  const Ti* const src[3] = {x, r, i};
+  const uint32_t pad[3] = {0u, minus_inf, 0u};
+  const Tu* const src_u[1] = {dh};
+  const uint32_t pad_u[1] = {0u};
   const auto fetch = [&](int j) {
-    char* st = ring + (j & 1) * kStage;
     if (j >= 0) {
-      const int t = first(j);
-      stage<Ti, MODE, kRun>(st, x, xp, t, t1, c0, D, total, 0, lane);
-      stage<Ti, MODE, kRun>(st + kArray, r, rp, t, t1, c0, D, total, minus_inf, lane);
-      stage<Ti, MODE, kRun>(st + 2 * kArray, i, ip, t, t1, c0, D, total, 0, lane);
-      stage<Tu, MODE, kRun>(st + 3 * kArray, dh, up, t, t1, c0, D, total, 0, lane);
-      xp -= stride;
-      rp -= stride;
-      ip -= stride;
-      up -= stride;
+      char* st = ring + j % kStages * kStage;
+      stage_rows<Ti, MODE, kRun>(st, src, pad, first(j), t1, c0, D, total, lane);
+      stage_rows<Tu, MODE, kRun>(st + 3 * kArray, src_u, pad_u, first(j), t1, c0, D, total, lane);
     }
     cp_commit();
   };
@@ -619,21 +600,20 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
   const auto run = [&](auto small) {
     for (int j = rounds - 1; j >= 0; --j) {
       const int n = rounds - 1 - j;
-      __syncwarp();                       // the buffer refilled now was read to the round's end
-      fetch(j - 1);
+      if (kStages > 1) fetch(j - 1);
       const F2 cs_next = entering(j - 1);
-      cp_wait<1>();
+      cp_wait<kStages - 1>();
       __syncwarp();
-      const char* st = ring + (j & 1) * kStage;
+      const char* st = ring + j % kStages * kStage;
       const int t = first(j);
       // the run's map of h forwards (fw) and of e backwards (the same product, sum w)
       F2 a[kRun], root[kRun], sr[kRun], si[kRun];
       Map fw = identity();
 #pragma unroll
       for (int k = 0; k < kRun; ++k) {
-        const F2 xv = row_pair<Ti, MODE>(st, k, t + k, c0, D, lane);
-        const F2 rv = row_pair<Ti, MODE>(st + kArray, k, t + k, c0, D, lane);
-        const F2 iv = row_pair<Ti, MODE>(st + 2 * kArray, k, t + k, c0, D, lane);
+        const F2 xv = row_pair<Ti, MODE>(st, k, t + k, D, lane);
+        const F2 rv = row_pair<Ti, MODE>(st + kArray, k, t + k, D, lane);
+        const F2 iv = row_pair<Ti, MODE>(st + 2 * kArray, k, t + k, D, lane);
         sr[k] = sigmoid(rv);
         si[k] = sigmoid(iv);
         decay<decltype(small)::value>(mul(ysc, sr[k]), a[k], root[k]);
@@ -643,8 +623,8 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
       F2 w = f2(0.f);
 #pragma unroll
       for (int k = kRun - 1; k >= 0; --k)
-        w = mul(a[k], add(row_pair<Tu, MODE>(st + 3 * kArray, k, t + k, c0, D, lane), w));
-      Maps* wm = ex.warp[n & 1];
+        w = mul(a[k], add(row_pair<Tu, MODE>(st + 3 * kArray, k, t + k, D, lane), w));
+      Maps* wm = warp_maps[n & 1];
       wm[warp][lane] = pack(Map{fw.A, w});
       wf[n & 1][warp][lane] = fw.V;
       __syncthreads();
@@ -676,19 +656,19 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
       }
       // the state before each token, kept where the token's gate inputs were (every lane has read
       // its own; odd rows share pieces, but all lanes are past the block barrier)
-      char* keep = ring + (j & 1) * kStage;
+      char* keep = ring + j % kStages * kStage;
 #pragma unroll
       for (int k = 0; k < kRun; ++k) {
         put_state<Ti, MODE>(keep, kArray, k, lane, hs);
-        const F2 xv = row_pair<Ti, MODE>(st, k, t + k, c0, D, lane);
+        const F2 xv = row_pair<Ti, MODE>(st, k, t + k, D, lane);
         if (k + 1 < kRun) hs = fma(a[k], hs, mul(mul(root[k], si[k]), xv));
       }
       const size_t at = static_cast<size_t>(t) * D + cA;
 #pragma unroll
       for (int k = kRun - 1; k >= 0; --k) {
-        const F2 xv = row_pair<Ti, MODE>(st, k, t + k, c0, D, lane);
+        const F2 xv = row_pair<Ti, MODE>(st, k, t + k, D, lane);
         const F2 hp = get_state<Ti, MODE>(keep, kArray, k, lane);
-        const F2 G = add(row_pair<Tu, MODE>(st + 3 * kArray, k, t + k, c0, D, lane), e);
+        const F2 G = add(row_pair<Tu, MODE>(st + 3 * kArray, k, t + k, D, lane), e);
         F2 gx, gr, gi, u;
         e = mul(a[k], G);
         gate_gradients(G, e, a[k], root[k], mul(ysc, sr[k]), sr[k], si[k], xv, hp, gx, gr, gi, u);
@@ -701,6 +681,8 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
         }
       }
       cs = cs_next;
+      __syncwarp();                       // the buffer refilled next was read to here
+      if (kStages == 1) fetch(j - 1);
     }
   };
   // every warp of the CTA has the same 64 channels, so all take the same way
@@ -1040,8 +1022,8 @@ cudaError_t launch_glr_fwd(const void* x, const void* r, const void* i, DType in
         using Ti = decltype(ti);
         using Th = decltype(th);
         constexpr int M = decltype(mode)::value;
-        const size_t smem = exchange_bytes(p.split) +
-                            kFwdStages * 3 * kFwdWarps * run_bytes<Ti, M, kFwdRun>();
+        const size_t smem = exchange_bytes(p.split, kFwdWarps) +
+                            stages<Ti>() * 3 * kFwdWarps * run_bytes<Ti, M, kFwdRun>();
         return launch_split(glr_fwd_kernel<Ti, Th, M>, kFwdWarps * 32, smem, blocks, p.split, s,
                             p, state_in,
                             state_out, static_cast<Th*>(h), chunk_states);
@@ -1085,8 +1067,8 @@ cudaError_t launch_glr_bwd(const void* x, const void* r, const void* i, DType in
           using Tg = decltype(tg);
           constexpr int M = decltype(mode)::value;
           const size_t smem =
-              exchange_bytes(p.split) + 2 * kBwdWarps * 32 * sizeof(F2) +
-              2 * kBwdWarps * (3 * run_bytes<Ti, M, kBwdRun>() + run_bytes<Tu, M, kBwdRun>());
+              exchange_bytes(p.split, kBwdWarps) + 2 * kBwdWarps * 32 * sizeof(F2) +
+              stages<Ti>() * kBwdWarps * (3 * run_bytes<Ti, M, kBwdRun>() + run_bytes<Tu, M, kBwdRun>());
           return launch_split(glr_bwd_kernel<Ti, Tu, Tg, M>, kBwdWarps * 32, smem, blocks,
                               p.split, s, p,
                               chunk_states, static_cast<const Tu*>(d_h), d_state_out,
