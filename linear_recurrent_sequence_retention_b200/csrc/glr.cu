@@ -16,14 +16,15 @@
 // enters each 64-token tile, which the forward stored.  The inputs of the next
 // round are copied to shared memory (cp.async) while the current one is computed.
 //
-// Measured at 2 x 8192 x 4096 bf16: forward 0.140 ms for 0.54 GB (59 % of the measured
-// copy rate), gradients 0.306 ms for 0.94 GB (47 %).  Neither HBM nor a pipe is full
+// Measured at 2 x 8192 x 4096 bf16: forward 0.141 ms for 0.54 GB (58 % of the measured
+// copy rate), gradients 0.273 ms for 0.94 GB (53 %).  Neither HBM nor a pipe is full
 // (special functions 55 %, issue 50 %): a round is a chain of ~2 us (gates, block barrier,
 // exchange, apply) and 128 (sequence, channel group) pairs give each SM only about two CTAs to
 // overlap, unevenly (256 CTAs on 148 SMs).  With 16 sequences of 1024 tokens, the same bytes, no
-// exchange and four CTAs per SM, the forward takes 0.108 ms (76 %).  Deeper prefetch (3 or 4
-// stages), 32-channel CTAs and computing the next round's gates before the exchange is awaited
-// changed the first case by less than 5 %.
+// exchange and a full SM, the times are 0.103 ms (80 %) and 0.223 ms (65 %).  Deeper prefetch (3 or
+// 4 stages), 32-channel CTAs, 8 warps of 8 tokens forward, results that leave through shared memory
+// in 16-byte pieces and computing the next round's gates before the exchange is awaited
+// changed the first case by less than 5 %, or made it slower.
 #include <cmath>
 #include <type_traits>
 
@@ -919,15 +920,16 @@ cudaError_t by_mode(bool any_bf16, int D, F&& f) {
   return f(std::integral_constant<int, kOdd>{});
 }
 
-// CTAs per cluster.  The busiest SM takes ceil(CTAs / SMs) of them (more than fit at once
-// follow one another), each ceil(tiles / S) rounds and about one more to start and end; a
-// round grows by ~4 % with each CTA whose map it waits for, an SM with a single CTA has
-// nothing to run meanwhile, and large clusters whose CTAs share SMs are slow.  Measured in
-// ms, forward / gradients: at 2 x 8192 x 4096 bf16 S = 1: 0.178/0.442, 2: 0.140/0.309, 6: 0.138/0.351,
-// 16: 0.173/0.433; at 1 x 16384 x 1024 S = 4: 0.119/0.242, 12: 0.060/0.124, 16: 0.058/0.158.
+// CTAs per cluster, from a model of the time in us.  A round takes a CTA about 1.4 + 0.1 S when
+// it is alone on its SM, and CTAs that share one bring it to 1.2 per round of each; a cluster
+// has ceil(tiles / S) rounds and about one more to start and end, and finds room the later the
+// larger it is (2 % per CTA, 30 % more where clusters of sixteen share SMs).  Sizes that are not
+// listed are placed badly.  Measured in us, forward / gradients: 2 x 8192 x 4096 bf16 S = 1:
+// 186/309, 2: 142/274, 4: 152/280, 7: 162/332, 16: 178/366; 1 x 16384 x 1024 S = 4: 120/186,
+// 8: 78/146, 12: 61/112, 14: 67/146, 16: 60/130; 1 x 1024 x 2048 S = 1: 26/43, 8: 9/15, 16: 11/20.
 // Packed sequences differ in length: the SMs share the average and the longest, taken as four
-// times the average, ends last (64 sequences, 200000 tokens x 1024: S = 1: 0.581, 4: 0.440,
-// 16: 0.625).
+// times the average, ends last (64 sequences, 200000 tokens x 1024: S = 1: 617/1263, 4: 404/827,
+// 16: 632/1302; 17 of 9001 x 1001 float32 S = 1: 98/193, 4: 54/99, 16: 89/188).
 constexpr double kSms = 148.0;
 int split_of(const SeqLayout& L, int D) {
   const double pairs = static_cast<double>((D + kChan - 1) / kChan) * L.nseq;
@@ -935,16 +937,18 @@ int split_of(const SeqLayout& L, int D) {
   const long long tiles = (L.Ttot + per - 1) / per;
   int best = 1;
   double cost = 0.0;
-  for (int s = 1; s <= kMaxSplit && (s == 1 || s <= tiles); ++s) {
+  for (const int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
+    if (s > 1 && s > tiles) break;
+    const double round = 1.4 + 0.1 * s;          // us
     double c;
     if (L.T > 0) {
       const double share = std::ceil(pairs * s / kSms);
-      c = share * static_cast<double>((tiles + s - 1) / s + 1) *
-          (share == 1.0 ? 1.5 : s > 12 ? 1.3 : 1.0);
+      c = static_cast<double>((tiles + s - 1) / s + 1) * std::fmax(round, 1.2 * share) *
+          (0.98 + 0.02 * s) * (s == kMaxSplit && share > 1.0 ? 1.3 : 1.0);
     } else {
-      c = pairs * static_cast<double>(tiles + s) / kSms + 4.0 * static_cast<double>(tiles) / s;
+      c = 1.2 * pairs * (static_cast<double>(tiles) + 1.5 * s) / kSms +
+          round * 4.0 * static_cast<double>(tiles) / s;
     }
-    c *= 1.0 + 0.04 * s;
     if (s == 1 || c < cost) {
       cost = c;
       best = s;
@@ -956,7 +960,7 @@ int split_of(const SeqLayout& L, int D) {
 // Whether threads walk their sequences alone: up to 32 tokens per sequence (16 on average where the
 // lengths differ, which the host does not know).  Measured in us, forward / gradients, alone
 // and by tiles: 256 x 4 x 4096 bf16 15 / 32 and 130 / 253, 32 x 16 x 2048 6.0 / 9.6 and 10.9 / 20.9,
-// 128 x 64 x 4096 77 / 196 and 74 / 169.
+// 128 x 64 x 4096 77 / 196 and 66 / 163.
 bool direct(const SeqLayout& L) {
   return L.Ttot <= (L.T > 0 ? 32ll : 16ll) * L.nseq;
 }
