@@ -673,6 +673,8 @@ def _current_raw_stream(device):
 def _new(stream, shape, dtype, like):
     """An uninitialised tensor that belongs to the stream the kernels will run on."""
     if stream is None:
+        if like.shape == shape:           # 1.3 us (another dtype: 1.6) instead of 2.0
+            return torch.empty_like(like, dtype=dtype) if like.dtype != dtype else torch.empty_like(like)
         return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
@@ -772,7 +774,7 @@ def glr_bwd(x, r, i, lam, chunk_states, d_h, c=8.0, cu_seqlens=None, d_state_out
     need = glr_bwd_workspace_size(B, T, D, nseq)
     gd = grad_dtype or x.dtype
     dx, dr, di = (_new(stream, x.shape, gd, x) for _ in range(3))
-    d_lam = _new(stream, (D,), torch.float32, x)
+    d_lam = _new(stream, (D,), torch.float32, lam)
     dS = _new(stream, states, torch.float32, x) if return_d_state else None
     if workspace is None:
         workspace = _new(stream, (need,), torch.uint8, x)
@@ -824,7 +826,8 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out_dtype=None, out=None
     if out is None:
         out = _new(stream, x.shape, out_dtype or x.dtype, x)
     if return_stats:
-        mean, rstd = (_new(stream, x.shape[:-1], torch.float32, x) for _ in range(2))
+        mean = _new(stream, x.shape[:-1], torch.float32, x)
+        rstd = _new(stream, x.shape[:-1], torch.float32, mean)
     st = lib().retention_layer_norm_fwd(_at(x), _dt(x), _at(weight), _at(bias), float(eps),
                                         _at(out), _dt(out), _at(mean), _at(rstd), ntok, D, raw)
     _check(st, "retention_layer_norm_fwd")
@@ -852,7 +855,8 @@ def layer_norm_bwd(x, d_y, mean, rstd, weight=None, return_d_affine=True, grad_d
     dw = db = None
     dx = _new(stream, x.shape, grad_dtype or x.dtype, x)
     if return_d_affine:
-        dw, db = (_new(stream, (D,), torch.float32, x) for _ in range(2))
+        dw = _new(stream, (D,), torch.float32, x if weight is None else weight)
+        db = _new(stream, (D,), torch.float32, dw)
         if workspace is None:
             workspace = _new(stream, (layer_norm_bwd_workspace_size(ntok, D),), torch.uint8, x)
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
@@ -886,9 +890,10 @@ def norm_gate_bwd(o, g, d_y, weight=None, bias=None, eps=1e-5, return_d_affine=T
             raise ValueError(f"{n} must be float32 with H*dv elements")
     dw = db = None
     gd = grad_dtype or d_y.dtype
-    d_o, d_g = _new(stream, o.shape, gd, o), _new(stream, g.shape, gd, o)
+    d_o, d_g = _new(stream, o.shape, gd, o), _new(stream, g.shape, gd, g)
     if return_d_affine:
-        dw, db = (_new(stream, (H * dv,), torch.float32, o) for _ in range(2))
+        dw = _new(stream, (H * dv,), torch.float32, o if weight is None else weight)
+        db = _new(stream, (H * dv,), torch.float32, dw)
         if workspace is None:
             workspace = _new(stream, (norm_gate_bwd_workspace_size(ntok, H, dv),), torch.uint8,
                              o)
