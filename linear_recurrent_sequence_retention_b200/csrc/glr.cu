@@ -342,7 +342,8 @@ __device__ __forceinline__ float4 pack(const Map& m) {
 struct Exchange {
   uint64_t bar[2];
   int abort;
-  int pad[3];
+  int seq;                              // of longest_first
+  int pad[2];
 };
 __host__ __device__ constexpr size_t exchange_bytes(int split, int warps) {
   return sizeof(Exchange) + 2 * (warps + (split > 1 ? split : 0)) * sizeof(Maps);
@@ -354,6 +355,37 @@ __device__ __forceinline__ void st_async_f32x4(uint32_t remote, float4 v, uint32
       "[%0], {%1, %2, %3, %4}, [%5];" ::"r"(remote),
       "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(remote_bar)
       : "memory");
+}
+
+// The sequence of a cluster that is the slot-th to start: packed sequences go by length, the longest
+// first (it ends last), where there are at most 128 of them; among more, one weighs less.  Every
+// cluster ranks them for itself.  17 sequences of 9001 tokens x 1001 float32, forward / gradients:
+// 42 / 84 us, in the given order 53 / 98.
+constexpr int kMaxRanked = 128;
+static_assert(kMaxRanked <= kFwdWarps * 32 && kMaxRanked <= kBwdWarps * 32, "a thread each");
+__device__ __forceinline__ int longest_first(const SeqLayout& L, int slot, Exchange& ex,
+                                             int* lengths) {
+  if (L.cu == nullptr || L.nseq == 1 || L.nseq > kMaxRanked) return slot;
+  const int s = threadIdx.x;
+  int mine = 0;
+  if (s == 0) ex.seq = slot;
+  if (s < L.nseq) {
+    int a, b;
+    seq_bounds(L, s, a, b);
+    lengths[s] = mine = b - a;
+  }
+  __syncthreads();
+  if (s < L.nseq) {
+    int before = 0;
+#pragma unroll 4
+    for (int q = 0; q < L.nseq; ++q) {
+      const int other = lengths[q];
+      before += other > mine || (other == mine && q < s);
+    }
+    if (before == slot) ex.seq = s;
+  }
+  __syncthreads();
+  return ex.seq;
 }
 
 // Start of a kernel: every CTA of the cluster is running and its barriers are set up
@@ -410,7 +442,8 @@ glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ s
   Maps* cta_maps = reinterpret_cast<Maps*>(warp_maps + 2);                // [2][S]
   char* ring = smem + exchange_bytes(S, kWarps) + warp * (kStages * 3 * kArray);
   const int pair = static_cast<int>(blockIdx.x / S);
-  const int seq = pair / p.groups, c0 = (pair % p.groups) * kChan;
+  const int seq = longest_first(p.L, pair / p.groups, ex, reinterpret_cast<int*>(warp_maps));
+  const int c0 = pair % p.groups * kChan;
   const int D = p.D;
   const int cA = c0 + (MODE == kOdd ? lane : 2 * lane), cB = MODE == kOdd ? cA + 32 : cA + 1;
   const bool okA = cA < D, okB = cB < D;
@@ -559,7 +592,8 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
   F2(*wf)[kWarps][32] = reinterpret_cast<F2(*)[kWarps][32]>(smem + exchange_bytes(S, kWarps));
   char* ring = reinterpret_cast<char*>(wf + 2) + warp * (kStages * kStage);
   const int pair = static_cast<int>(blockIdx.x / S);
-  const int seq = pair / p.groups, c0 = (pair % p.groups) * kChan;
+  const int seq = longest_first(p.L, pair / p.groups, ex, reinterpret_cast<int*>(warp_maps));
+  const int c0 = pair % p.groups * kChan;
   const int D = p.D;
   const int cA = c0 + (MODE == kOdd ? lane : 2 * lane), cB = MODE == kOdd ? cA + 32 : cA + 1;
   const bool okA = cA < D, okB = cB < D;
@@ -927,9 +961,11 @@ cudaError_t by_mode(bool any_bf16, int D, F&& f) {
 // listed are placed badly.  Measured in us, forward / gradients: 2 x 8192 x 4096 bf16 S = 1:
 // 186/309, 2: 142/274, 4: 152/280, 7: 162/332, 16: 178/366; 1 x 16384 x 1024 S = 4: 120/186,
 // 8: 78/146, 12: 61/112, 14: 67/146, 16: 60/130; 1 x 1024 x 2048 S = 1: 26/43, 8: 9/15, 16: 11/20.
-// Packed sequences differ in length: the SMs share the average and the longest, taken as four
-// times the average, ends last (64 sequences, 200000 tokens x 1024: S = 1: 617/1263, 4: 404/827,
-// 16: 632/1302; 17 of 9001 x 1001 float32 S = 1: 98/193, 4: 54/99, 16: 89/188).
+// Packed sequences differ in length, which the host does not know: the SMs share the sum, each
+// cluster rounded up and started, while the longest, taken as four times the average, goes on
+// alone (64 sequences, 200000 tokens x 1024: S = 1: 509/832, 2: 362/694, 4: 387/785, 16: 684/1363;
+// 17 of 9001 x 1001 float32 S = 1: 98/169, 3: 50/84, 16: 96/194; 40 of 20000 x 2048 bf16 S = 1:
+// 76/146, 4: 125/234).
 constexpr double kSms = 148.0;
 int split_of(const SeqLayout& L, int D) {
   const double pairs = static_cast<double>((D + kChan - 1) / kChan) * L.nseq;
@@ -946,8 +982,9 @@ int split_of(const SeqLayout& L, int D) {
       c = static_cast<double>((tiles + s - 1) / s + 1) * std::fmax(round, 1.2 * share) *
           (0.98 + 0.02 * s) * (s == kMaxSplit && share > 1.0 ? 1.3 : 1.0);
     } else {
-      c = 1.2 * pairs * (static_cast<double>(tiles) + 1.5 * s) / kSms +
-          round * 4.0 * static_cast<double>(tiles) / s;
+      const double sum = 1.2 * pairs * (static_cast<double>(tiles) + 1.5 * s) / kSms;
+      const double longest = round * std::fmin(4.0, L.nseq) * static_cast<double>(tiles) / s;
+      c = std::fmax(sum, longest) + 0.2 * std::fmin(sum, longest);
     }
     if (s == 1 || c < cost) {
       cost = c;

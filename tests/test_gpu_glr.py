@@ -418,3 +418,30 @@ def test_binding_refusals():
     flat = torch.zeros(2 * 8 * 16 + 1, device="cuda")[1:].view(2, 8, 16)      # 4 bytes off 16
     with pytest.raises(ops.RetentionError):
         ops.glr_fwd(flat, r, i, lam)
+
+
+@pytest.mark.parametrize("lens", [[70] * 128, [64 * (s % 7) + s % 3 for s in range(128)],
+                                  [s % 90 for s in range(129)], [900] + [20] * 60 + [901]],
+                         ids=["128equal", "128ties", "129given", "62ends"])
+def test_sequences_that_start_in_another_order(lens):
+    """Up to 128 packed sequences start longest first, more in their own order: equal lengths, empty
+    ones and the longest at either end keep their states apart, and calls repeat."""
+    D = 72
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    T = int(cu[-1])
+    x, r, i, lam, dh, S0, dS = make(1, T, D, "f32", nstate=len(lens), seed=len(lens))
+    ref = Reference(x, r, i, lam, dh, S0, dS, cu)
+    xd, rd, id_, ld, dhd, S0d, dSd = cuda(x, r, i, lam, dh, S0, dS)
+    cud = torch.from_numpy(cu).cuda()
+
+    def run():
+        h, S, chunks = ops.glr_fwd(xd, rd, id_, ld, cu_seqlens=cud, state_in=S0d,
+                                   return_state=True, return_chunks=True)
+        return (h, S, chunks) + ops.glr_bwd(xd, rd, id_, ld, chunks, dhd, cu_seqlens=cud,
+                                            d_state_out=dSd, return_d_state=True)
+    out = run()
+    ref.check_forward(*out[:2], T, out[2], cu)
+    ref.check_gradients(out[3:], T)
+    again = run()
+    assert all(torch.equal(a, b) for a, b in zip(out[:2] + out[3:], again[:2] + again[3:]))
+    ops.check_device_error()
