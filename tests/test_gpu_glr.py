@@ -162,6 +162,21 @@ def test_gradients_of_mixed_types(dtype, up, out, D):
     ops.check_device_error()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [33, 64, 129, 1100])
+@pytest.mark.parametrize("D", [1, 2, 3, 7, 8, 65])
+def test_few_channels(dtype, T, D):
+    """Rows shorter than a 16-byte piece share it with others; the tensor's last piece is cut."""
+    x, r, i, lam, dh, S0, dS = make(1, T, D, dtype, seed=T + D)
+    ref = Reference(x, r, i, lam, dh, S0, dS)
+    xd, rd, id_, ld, dhd, S0d, dSd = cuda(x, r, i, lam, dh, S0, dS)
+    h, S, chunks = ops.glr_fwd(xd, rd, id_, ld, state_in=S0d, return_state=True, return_chunks=True)
+    ref.check_forward(h, S, T, chunks)
+    got = ops.glr_bwd(xd, rd, id_, ld, chunks, dhd, d_state_out=dSd, return_d_state=True)
+    ref.check_gradients(got, T)
+    ops.check_device_error()
+
+
 PACKED = [[0, 1, 64, 65, 0, 300, 127], [5], [0, 0], [1] * 40, [3, 0, 0, 2, 1, 0] * 30, [700, 1, 1200]]
 
 
