@@ -16,8 +16,8 @@
 // enters each 64-token tile, which the forward stored.  The inputs of the next
 // round are copied to shared memory (cp.async) while the current one is computed.
 //
-// Measured at 2 x 8192 x 4096 bf16: forward 0.141 ms for 0.54 GB (58 % of the measured
-// copy rate), gradients 0.273 ms for 0.94 GB (53 %).  Neither HBM nor a pipe is full
+// Measured at 2 x 8192 x 4096 bf16: forward 0.140 ms for 0.54 GB (59 % of the measured
+// copy rate), gradients 0.268 ms for 0.94 GB (54 %).  Neither HBM nor a pipe is full
 // (special functions 55 %, issue 50 %): a round is a chain of ~2 us (gates, block barrier,
 // exchange, apply) and 128 (sequence, channel group) pairs give each SM only about two CTAs to
 // overlap, unevenly (256 CTAs on 148 SMs).  With 16 sequences of 1024 tokens, the same bytes, no
@@ -664,9 +664,8 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
       wf[n & 1][warp][lane] = fw.V;
       __syncthreads();
       F2 hs = cs, e;                      // the state and the gradient that enter the run
-#pragma unroll
-      for (int q = 0; q < kWarps - 1; ++q)
-        if (q < warp) hs = fma(get(wm[q], lane).A, hs, wf[n & 1][q][lane]);
+#pragma unroll 1
+      for (int q = 0; q < warp; ++q) hs = fma(get(wm[q], lane).A, hs, wf[n & 1][q][lane]);
       if (S == 1) {
         e = carry;
 #pragma unroll
@@ -676,9 +675,8 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
         }
       } else {
         Map after = identity();
-#pragma unroll
-        for (int q = kWarps - 1; q > 0; --q)
-          if (q > warp) after = then(after, get(wm[q], lane));
+#pragma unroll 1
+        for (int q = kWarps - 1; q > warp; --q) after = then(after, get(wm[q], lane));
         if (warp == 0) send(ex, cta_maps, then(after, Map{fw.A, w}), n, S, rank, lane);
         receive(ex, n, p.err);
         const Maps* cm = cta_maps + (n & 1) * S;
