@@ -62,6 +62,23 @@ __device__ __forceinline__ F2 f2(float x) { return make_float2(x, x); }
 __device__ __forceinline__ F2 mul(F2 a, F2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ F2 add(F2 a, F2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) { return __ffma2_rn(a, b, c); }
+// The same, or one instruction per channel: the gradients of float32 rows, and of bf16 rows whose
+// channels come apart (kOdd), need fewer registers and are faster so, 0.190 ms instead of 0.197 ms at 2 x 8192 x 2048 (bf16: 0.283
+// instead of 0.270 ms at 2 x 8192 x 4096; the forward: 0.104 instead of 0.096 ms float32).
+template <bool PACKED> struct Pairs {
+  static __device__ __forceinline__ F2 mul(F2 a, F2 b) {
+    if constexpr (PACKED) return __fmul2_rn(a, b);
+    return make_float2(a.x * b.x, a.y * b.y);
+  }
+  static __device__ __forceinline__ F2 add(F2 a, F2 b) {
+    if constexpr (PACKED) return __fadd2_rn(a, b);
+    return make_float2(a.x + b.x, a.y + b.y);
+  }
+  static __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+    if constexpr (PACKED) return __ffma2_rn(a, b, c);
+    return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
+  }
+};
 
 // ---- gates -----------------------------------------------------------------
 
@@ -191,7 +208,7 @@ template <typename T, int MODE> __device__ __forceinline__ int row_shift(int t, 
 // run_bytes after the other; rows at or past t1 are filled with `fill` (two bf16, or the float)
 // instead: r = -inf, and zeros elsewhere, make a token the identity.  `total` is the tensor's
 // element count: nothing past it is read.  (4-byte pieces, which fit every row, took 0.147 ms
-// instead of 0.052 ms forward and 0.182 instead of 0.098 ms backward at 8192 x 1001 bf16.)
+// instead of 0.052 ms forward and 0.182 instead of 0.098 ms for the gradients at 8192 x 1001 bf16.)
 template <typename T, int MODE, int RUN, int N>
 __device__ __forceinline__ void stage_rows(char* dst, const T* const (&src)[N],
                                            const uint32_t (&fill)[N], int t, int t1, int c0, int D,
@@ -360,7 +377,7 @@ __device__ __forceinline__ void st_async_f32x4(uint32_t remote, float4 v, uint32
 // The sequence of a cluster that is the slot-th to start: packed sequences go by length, the longest
 // first (it ends last), where there are at most 128 of them; among more, one weighs less.  Every
 // cluster ranks them for itself.  17 sequences of 9001 tokens x 1001 float32, forward / gradients:
-// 42 / 84 us, in the given order 53 / 98.
+// 42 / 84 us in this order, 53 / 98 in the given one (clusters of four).
 constexpr int kMaxRanked = 128;
 static_assert(kMaxRanked <= kFwdWarps * 32 && kMaxRanked <= kBwdWarps * 32, "a thread each");
 __device__ __forceinline__ int longest_first(const SeqLayout& L, int slot, Exchange& ex,
@@ -563,15 +580,16 @@ glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ s
 // ---- gradients -------------------------------------------------------------
 
 // A token's gradients from G = d_h + e, the e it passes on (a G) and the state before it.
+template <typename P>
 __device__ __forceinline__ void gate_gradients(F2 G, F2 e, F2 a, F2 root, F2 y, F2 sr, F2 si, F2 x,
                                                F2 hp, F2& gx, F2& gr, F2& gi, F2& u) {
   // 1 / root; where root is zero y is below 1e-38 and y / root counts as zero either way
   const F2 inv = make_float2(rcp_approx(fmaxf(root.x, 1e-19f)), rcp_approx(fmaxf(root.y, 1e-19f)));
-  const F2 six = mul(si, x), ai = mul(a, inv);
-  gx = mul(G, mul(root, si));
-  const F2 gix = mul(gx, x);
+  const F2 six = P::mul(si, x), ai = P::mul(a, inv);
+  gx = P::mul(G, P::mul(root, si));
+  const F2 gix = P::mul(gx, x);
   gi = make_float2(fmaf(gix.x, -si.x, gix.x), fmaf(gix.y, -si.y, gix.y));
-  u = mul(mul(e, y), make_float2(fmaf(ai.x, six.x, -hp.x), fmaf(ai.y, six.y, -hp.y)));
+  u = P::mul(P::mul(e, y), make_float2(fmaf(ai.x, six.x, -hp.x), fmaf(ai.y, six.y, -hp.y)));
   gr = make_float2(fmaf(u.x, -sr.x, u.x), fmaf(u.y, -sr.y, u.y));
 }
 
@@ -581,6 +599,7 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
                const float* __restrict__ d_state_out, Tg* __restrict__ dx, Tg* __restrict__ dr,
                Tg* __restrict__ di, float* __restrict__ d_state_in, float* __restrict__ partial) {
   extern __shared__ __align__(16) char smem[];
+  using P = Pairs<sizeof(Ti) == 2 && MODE != kOdd>;
   constexpr int kWarps = kBwdWarps, kRun = kBwdRun;
   constexpr int kArray = run_bytes<Ti, MODE, kRun>(), kUp = run_bytes<Tu, MODE, kRun>();
   constexpr int kStage = 3 * kArray + kUp, kStages = stages<Ti>();
@@ -651,21 +670,21 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
         const F2 iv = row_pair<Ti, MODE>(st + 2 * kArray, k, t + k, D, lane);
         sr[k] = sigmoid(rv);
         si[k] = sigmoid(iv);
-        decay<decltype(small)::value>(mul(ysc, sr[k]), a[k], root[k]);
-        const Map m = Map{a[k], mul(mul(root[k], si[k]), xv)};
+        decay<decltype(small)::value>(P::mul(ysc, sr[k]), a[k], root[k]);
+        const Map m = Map{a[k], P::mul(P::mul(root[k], si[k]), xv)};
         fw = k == 0 ? m : then(fw, m);
       }
       F2 w = f2(0.f);
 #pragma unroll
       for (int k = kRun - 1; k >= 0; --k)
-        w = mul(a[k], add(row_pair<Tu, MODE>(st + 3 * kArray, k, t + k, D, lane), w));
+        w = P::mul(a[k], P::add(row_pair<Tu, MODE>(st + 3 * kArray, k, t + k, D, lane), w));
       Maps* wm = warp_maps[n & 1];
       wm[warp][lane] = pack(Map{fw.A, w});
       wf[n & 1][warp][lane] = fw.V;
       __syncthreads();
       F2 hs = cs, e;                      // the state and the gradient that enter the run
 #pragma unroll 1
-      for (int q = 0; q < warp; ++q) hs = fma(get(wm[q], lane).A, hs, wf[n & 1][q][lane]);
+      for (int q = 0; q < warp; ++q) hs = P::fma(get(wm[q], lane).A, hs, wf[n & 1][q][lane]);
       if (S == 1) {
         e = carry;
 #pragma unroll
@@ -694,18 +713,19 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
       for (int k = 0; k < kRun; ++k) {
         put_state<Ti, MODE>(keep, kArray, k, lane, hs);
         const F2 xv = row_pair<Ti, MODE>(st, k, t + k, D, lane);
-        if (k + 1 < kRun) hs = fma(a[k], hs, mul(mul(root[k], si[k]), xv));
+        if (k + 1 < kRun) hs = P::fma(a[k], hs, P::mul(P::mul(root[k], si[k]), xv));
       }
       const size_t at = static_cast<size_t>(t) * D + cA;
 #pragma unroll
       for (int k = kRun - 1; k >= 0; --k) {
         const F2 xv = row_pair<Ti, MODE>(st, k, t + k, D, lane);
         const F2 hp = get_state<Ti, MODE>(keep, kArray, k, lane);
-        const F2 G = add(row_pair<Tu, MODE>(st + 3 * kArray, k, t + k, D, lane), e);
+        const F2 G = P::add(row_pair<Tu, MODE>(st + 3 * kArray, k, t + k, D, lane), e);
         F2 gx, gr, gi, u;
-        e = mul(a[k], G);
-        gate_gradients(G, e, a[k], root[k], mul(ysc, sr[k]), sr[k], si[k], xv, hp, gx, gr, gi, u);
-        usum = add(usum, u);
+        e = P::mul(a[k], G);
+        gate_gradients<P>(G, e, a[k], root[k], P::mul(ysc, sr[k]), sr[k], si[k], xv, hp, gx, gr, gi,
+                          u);
+        usum = P::add(usum, u);
         if (t + k < t1) {
           const size_t o = at + static_cast<size_t>(k) * D;
           store_pair<Tg, MODE>(dx + o, gx, okA, okB);
@@ -730,7 +750,7 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
   __syncthreads();
   if (warp == 0) {
 #pragma unroll
-    for (int q = 1; q < kWarps; ++q) usum = add(usum, wf[0][q][lane]);
+    for (int q = 1; q < kWarps; ++q) usum = P::add(usum, wf[0][q][lane]);
     store2(partial, (static_cast<size_t>(seq) * S + rank) * D, usum, cA, cB, D);
   }
   exchange_end(S);
@@ -886,8 +906,8 @@ glr_bwd_direct_kernel(Args p, const float* __restrict__ chunk_states, const Tu* 
         const F2 G = add(uv[k], e);
         F2 gx, gr, gi, u;
         e = mul(a[k], G);
-        gate_gradients(G, e, a[k], root[k], mul(ysc, sr[k]), sr[k], si[k], xv[k], hp[k], gx, gr, gi,
-                       u);
+        gate_gradients<Pairs<true>>(G, e, a[k], root[k], mul(ysc, sr[k]), sr[k], si[k], xv[k],
+                                    hp[k], gx, gr, gi, u);
         usum = add(usum, u);
         const size_t o = at + static_cast<size_t>(k) * D;
         store_two<Tg, PAIR>(dx + o, gx, true, okB);
