@@ -63,8 +63,9 @@ __device__ __forceinline__ F2 mul(F2 a, F2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ F2 add(F2 a, F2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) { return __ffma2_rn(a, b, c); }
 // The same, or one instruction per channel: the gradients of float32 rows, and of bf16 rows whose
-// channels come apart (kOdd), need fewer registers and are faster so, 0.190 ms instead of 0.197 ms at 2 x 8192 x 2048 (bf16: 0.283
-// instead of 0.270 ms at 2 x 8192 x 4096; the forward: 0.104 instead of 0.096 ms float32).
+// channels come apart (kOdd), need fewer registers and are faster so, 0.190 ms instead of 0.197 ms
+// at 2 x 8192 x 2048 float32.  Packed, bf16 takes 0.268 instead of 0.283 ms at 2 x 8192 x 4096, and
+// the forward 0.096 instead of 0.104 ms at 2 x 8192 x 2048 float32.
 template <bool PACKED> struct Pairs {
   static __device__ __forceinline__ F2 mul(F2 a, F2 b) {
     if constexpr (PACKED) return __fmul2_rn(a, b);
@@ -1127,7 +1128,8 @@ cudaError_t launch_glr_bwd(const void* x, const void* r, const void* i, DType in
           constexpr int M = decltype(mode)::value;
           const size_t smem =
               exchange_bytes(p.split, kBwdWarps) + 2 * kBwdWarps * 32 * sizeof(F2) +
-              stages<Ti>() * kBwdWarps * (3 * run_bytes<Ti, M, kBwdRun>() + run_bytes<Tu, M, kBwdRun>());
+              stages<Ti>() * kBwdWarps *
+                  (3 * run_bytes<Ti, M, kBwdRun>() + run_bytes<Tu, M, kBwdRun>());
           return launch_split(glr_bwd_kernel<Ti, Tu, Tg, M>, kBwdWarps * 32, smem, blocks,
                               p.split, s, p,
                               chunk_states, static_cast<const Tu*>(d_h), d_state_out,
