@@ -516,8 +516,9 @@ RET_API ret_status msr_norm_gate(const void* o, ret_dtype o_dtype, const ret_nor
  *          chunks of sequence s, which starts at flat token n, are the rows
  *          n / RETENTION_GLR_CHUNK + s, and on; rows between two sequences may
  *          stay unwritten.
- * All arithmetic is float32, whatever the inputs' type; h is rounded once when
- * it is stored as bf16.  1 - a^2 is formed without cancellation for decays near
+ * All arithmetic is float32, whatever the inputs' type (c softplus(lam) beyond
+ * the largest float counts as it, and s_t below the smallest normal one as
+ * zero); h is rounded once when it is stored as bf16.  1 - a^2 is formed without cancellation for decays near
  * one.  No workspace.  Inconsistent cu_seqlens are clamped and reported as
  * RET_ERR_DEVICE_DATA.
  * Supported: any T (packed T = 0 included) with B*T + 2048 < 2^31, D in 1..2^20;

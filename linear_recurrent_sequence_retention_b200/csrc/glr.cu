@@ -115,6 +115,16 @@ __device__ __forceinline__ float sigmoid(float x) {
 }
 __device__ __forceinline__ F2 sigmoid(F2 x) { return make_float2(sigmoid(x.x), sigmoid(x.y)); }
 
+// c softplus(lam), at most the largest float: an infinite scale times the sigmoid of a closed gate
+// (r = -inf, which also fills the last tile) or times a decay of zero would be NaN.  sigmoid never
+// exceeds one, so y stays finite.
+__device__ __forceinline__ float gate_scale(float c, float lam) {
+  return min_nan(c * softplus(lam), 3.402823466e38f);
+}
+__device__ __forceinline__ F2 gate_scale(float c, F2 lam) {
+  return make_float2(gate_scale(c, lam.x), gate_scale(c, lam.y));
+}
+
 // a = exp(-y) and root = sqrt(1 - a^2) for y >= 0, both to a few units of their
 // own last place.  y = n ln 2 + g, |g| <= ln 2 / 2, and with w = 1 - e^-g = g + g^2 q(g)
 // (q: the degree-4 polynomial of least largest error, found by reweighted least squares
@@ -498,7 +508,7 @@ glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ s
   };
   fetch(0);
   const F2 lm = load2(p.lam, 0, cA, cB, D);
-  const F2 ysc = make_float2(p.c * softplus(lm.x), p.c * softplus(lm.y));
+  const F2 ysc = gate_scale(p.c, lm);
   F2 carry = load2(state_in, static_cast<size_t>(seq) * D, cA, cB, D);
   exchange_begin(ex, S);
   const auto run = [&](auto small) {
@@ -647,7 +657,7 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
   fetch(rounds - 1);
   F2 cs = entering(rounds - 1);
   const F2 lm = load2(p.lam, 0, cA, cB, D);
-  const F2 ysc = make_float2(p.c * softplus(lm.x), p.c * softplus(lm.y));
+  const F2 ysc = gate_scale(p.c, lm);
   const size_t so = static_cast<size_t>(seq) * D;
   F2 carry = load2(d_state_out, so, cA, cB, D);
   F2 usum = f2(0.f);
@@ -808,7 +818,7 @@ glr_fwd_direct_kernel(Args p, const float* __restrict__ state_in, float* __restr
   int t0, t1;
   seq_bounds(p.L, seq, t0, t1);
   const F2 lm = load2(p.lam, 0, cA, cB, D);
-  const F2 ysc = make_float2(p.c * softplus(lm.x), p.c * softplus(lm.y));
+  const F2 ysc = gate_scale(p.c, lm);
   F2 st = load2(state_in, static_cast<size_t>(seq) * D, cA, cB, D);
   size_t at = static_cast<size_t>(t0) * D + cA;
   for (int t = t0; t < t1; t += kBatch) {
@@ -858,7 +868,7 @@ glr_bwd_direct_kernel(Args p, const float* __restrict__ chunk_states, const Tu* 
   int t0, t1;
   seq_bounds(p.L, seq, t0, t1);
   const F2 lm = load2(p.lam, 0, cA, cB, D);
-  const F2 ysc = make_float2(p.c * softplus(lm.x), p.c * softplus(lm.y));
+  const F2 ysc = gate_scale(p.c, lm);
   const size_t so = static_cast<size_t>(seq) * D;
   F2 e = load2(d_state_out, so, cA, cB, D), usum = f2(0.f);
   F2 enter[kGlrChunk / kBatch];           // the state before each batch of the chunk
@@ -952,7 +962,7 @@ glr_step_kernel(const Ti* __restrict__ x, const Ti* __restrict__ r, const Ti* __
   if (d >= D) return;
   const size_t at = static_cast<size_t>(blockIdx.x / groups) * D + d;
   float a, root;
-  decay<false>(c * softplus(lam[d]) * sigmoid(Io<Ti>::ld(r, at)), a, root);
+  decay<false>(gate_scale(c, lam[d]) * sigmoid(Io<Ti>::ld(r, at)), a, root);
   const float st = fmaf(a, state[at], root * sigmoid(Io<Ti>::ld(i, at)) * Io<Ti>::ld(x, at));
   state_out[at] = st;
   if (h) Io<Th>::st(h, at, st);
