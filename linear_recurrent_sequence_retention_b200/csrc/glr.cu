@@ -931,6 +931,14 @@ glr_bwd_direct_kernel(Args p, const float* __restrict__ chunk_states, const Tu* 
   store2(partial, so, usum, cA, cB, D);
 }
 
+// With t = exp(-|x|): 1 / ((1 + t) (x + log1p(t))) for x > 0, t / ((1 + t) log1p(t)) otherwise, so
+// that no exponential overflows.  The second tends to one as t vanishes.
+__device__ __forceinline__ float sigmoid_over_softplus(float x) {
+  const float t = expf(-fabsf(x));
+  if (x > 0.f) return 1.0f / ((1.0f + t) * (x + log1pf(t)));
+  return t == 0.f ? 1.f : t / ((1.0f + t) * log1pf(t));
+}
+
 // d_lam = (sum of the partial rows) sigmoid(lam) / softplus(lam).  32 channels
 // per block; eight row groups, each in order, then the groups in order.
 __global__ void __launch_bounds__(256)
@@ -946,9 +954,7 @@ glr_dlam_kernel(const float* __restrict__ partial, const float* __restrict__ lam
   __syncthreads();
   if (g > 0 || d >= D) return;
   for (int k = 1; k < 8; ++k) s += part[k][lane];
-  // the ratio tends to one as both underflow
-  const float sp = softplus(lam[d]);
-  d_lam[d] = s * (sp > 0.f ? 1.0f / ((1.0f + expf(-lam[d])) * sp) : 1.f);
+  d_lam[d] = s * sigmoid_over_softplus(lam[d]);
 }
 
 // ---- one token -------------------------------------------------------------

@@ -66,3 +66,42 @@ def test_gate_of_nan_stays_nan():
     got = ops.glr_bwd(x, r, i, lam, chunks, dh)
     assert all(torch.isnan(g[..., 5]).all() for g in got)
     assert all(torch.isfinite(g[..., keep]).all() for g in got)
+
+
+@pytest.mark.parametrize("T", [9, 40])
+def test_lam_whose_exponential_is_subnormal(T):
+    """sigmoid(lam) / softplus(lam) tends to one from below zero on, also where exp(-lam) is
+    infinite in float32 (lam < -88.7).  A large c makes such channels count.  softplus(lam) is
+    then subnormal: at lam >= -89.5 it is off by at most two of 2^-149, 2.1e-6 of itself, which
+    every bound below leaves room for."""
+    c = 1e38
+    x, r, i, lam, dh, S0, dS = make(2, T, 24, seed=T)
+    lam[:] = torch.linspace(-89.5, -85.0, 24)
+    # the oracle at its default c and the lam that gives the same decays; d_lam / d(c softplus)
+    # differs by the factors, the one here being one to 1e-37
+    scale = c * np.exp(W.to_f64(lam))
+    same = np.log(np.expm1(scale / C))
+    ref = Reference(x, r, i, torch.from_numpy(same), dh, S0, dS)
+    factor = (1 + np.exp(-same)) * scale / C
+    ref.dlam, ref.dlam_size = ref.dlam * factor, ref.dlam_size * factor
+    args = cuda(x, r, i, lam, dh, S0, dS)
+    h, S, chunks = ops.glr_fwd(*args[:4], c=c, state_in=args[5], return_state=True, return_chunks=True)
+    ref.check_forward(h, S, T, chunks)
+    ref.check_gradients(ops.glr_bwd(*args[:4], chunks, args[4], c=c, d_state_out=args[6],
+                                    return_d_state=True), T)
+
+
+def test_d_lam_is_the_sum_of_dr_for_any_negative_lam():
+    """Below lam = -20 the factor is one, and d_lam = sum u = sum dr / (1 - s): float32 sums of 80
+    terms (1e-5 of the terms' sizes), whatever softplus(lam) has been rounded to."""
+    x, r, i, lam, dh, S0, dS = make(2, 40, 64, seed=1)
+    lam[:] = torch.linspace(-103.0, -20.0, 64)
+    args = cuda(x, r, i, lam, dh, S0, dS)
+    for c in (8.0, 1e20, 1e38):
+        h, chunks = ops.glr_fwd(*args[:4], c=c, state_in=args[5], return_chunks=True)
+        _, dr, _, d_lam = ops.glr_bwd(*args[:4], chunks, args[4], c=c)
+        u = W.to_f64(dr) * (1 + np.exp(W.to_f64(r)))
+        err = np.abs(W.to_f64(d_lam) - u.sum(axis=(0, 1)))
+        size = np.abs(u).sum(axis=(0, 1))
+        assert np.all(err <= 1e-5 * size + 1e-36), (c, (err / (size + 1e-36)).max())
+        assert c < 1e38 or np.all(size[W.to_f64(lam) < -88.7] > 1e-5)
