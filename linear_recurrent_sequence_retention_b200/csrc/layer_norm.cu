@@ -438,8 +438,8 @@ constexpr bool any_width(int tpr, int ch) {
 int bwd_blocks(const Shape& s, int ntok) {
   const int groups = bwd_threads(s.tpr) / s.tpr;
   const int per_sm = s.vec ? bwd_blocks_per_sm(s.tpr) : s.tpr > 256 ? 1 : 4;
-  const int need = (ntok + groups - 1) / groups;
-  return need < kSms * per_sm ? need : kSms * per_sm;
+  const long long need = (static_cast<long long>(ntok) + groups - 1) / groups;
+  return need < kSms * per_sm ? static_cast<int>(need) : kSms * per_sm;
 }
 
 }  // namespace
