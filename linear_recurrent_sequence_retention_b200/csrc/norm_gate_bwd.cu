@@ -83,7 +83,7 @@ ng_bwd_kernel(const To* __restrict__ o, const Ti* __restrict__ g, const Ti* __re
     for (int e = 0; e < VEC; ++e) dw[k][e] = db[k][e] = 0.f;
   const float invD = 1.0f / dv;
   // all groups of a warp take the same number of turns (the sums are warp-wide shuffles)
-  const int turns = (ntok + lanes - 1) / lanes;
+  const int turns = static_cast<int>((static_cast<long long>(ntok) + lanes - 1) / lanes);
   int use = 0, fill = kStages - 1;
   long long n = first;
   for (int it = 0; it < turns; ++it) {

@@ -43,3 +43,15 @@ def test_layer_norm_gradients_of_the_most_tokens():
     assert torch.equal(dx[whole:], want[:MOST - whole])
     only = ops.layer_norm_bwd(x, dy, mean, rstd, return_d_affine=False)
     assert torch.equal(only[whole - 4099:whole], want) and torch.equal(only[whole:], want[:MOST - whole])
+
+
+def test_norm_gate_gradients_of_the_most_tokens():
+    """2^31 - 1 rows of eight channels (34 GB a tensor; o, g and d_y are one)."""
+    o, rows = _pattern(MOST, 1, 8)
+    want = ops.norm_gate_bwd(rows, rows, rows, return_d_affine=False)
+    got = ops.norm_gate_bwd(o, o, o, return_d_affine=False)
+    whole = MOST // 4099 * 4099
+    for g, w in zip(got, want):
+        for first in (0, 4099 * 1000, whole - 4099):
+            assert torch.equal(g[first:first + 4099], w)
+        assert torch.equal(g[whole:], w[:MOST - whole])
