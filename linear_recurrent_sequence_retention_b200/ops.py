@@ -217,6 +217,16 @@ def _dt(t):
     raise TypeError(f"unsupported dtype {t.dtype} (float32 or bfloat16)")
 
 
+def _wide(sizes):
+    """Whether one of the or-ed sizes is negative or past a C int, of which ctypes would pass the
+    low 32 bits."""
+    return sizes >> 31
+
+
+def _too_large(where):
+    return RetentionError(RET_ERR_INVALID_ARG, where)
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -701,10 +711,10 @@ def _offsets(cu_seqlens):
 
 def glr_chunk_slots(B, T, nseq=0):
     """Rows of ``chunk_states`` for these sizes (0 if they are invalid)."""
-    return int(lib().retention_glr_chunk_slots(B, T, nseq))
+    return int(lib().retention_glr_chunk_slots(B, T, nseq)) if not _wide(B | T | nseq) else 0
 
 
-def _glr_inputs(x, r, i, lam, cu_seqlens):
+def _glr_inputs(where, x, r, i, lam, cu_seqlens):
     if x.dim() != 3 or r.shape != x.shape or i.shape != x.shape or not x.dtype == r.dtype == i.dtype:
         raise ValueError("x, r, i must have one [B,T,D] shape and one dtype")
     B, T, D = x.shape
@@ -712,6 +722,8 @@ def _glr_inputs(x, r, i, lam, cu_seqlens):
     nseq = _offsets(cu_seqlens)
     if nseq and B != 1:
         raise ValueError("packed sequences need B = 1")
+    if _wide(B | T | D | nseq):
+        raise _too_large(where)
     return B, T, D, nseq
 
 
@@ -728,7 +740,7 @@ def glr_fwd(x, r, i, lam, c=8.0, cu_seqlens=None, state_in=None, return_state=Fa
     """
     raw = _ready(stream, x=x, r=r, i=i, lam=lam, cu_seqlens=cu_seqlens, state_in=state_in, out=out,
                  state_out=state_out, chunk_states=chunk_states)
-    B, T, D, nseq = _glr_inputs(x, r, i, lam, cu_seqlens)
+    B, T, D, nseq = _glr_inputs("retention_glr_fwd", x, r, i, lam, cu_seqlens)
     states = (nseq or B, D)
     slots = (glr_chunk_slots(B, T, nseq), D) if return_chunks or chunk_states is not None else None
     _shaped(state_in, "state_in", states, torch.float32)
@@ -752,6 +764,8 @@ def glr_fwd(x, r, i, lam, c=8.0, cu_seqlens=None, state_in=None, return_state=Fa
 
 
 def glr_bwd_workspace_size(B, T, D, nseq=0):
+    if _wide(B | T | D | nseq):
+        return 0
     return int(lib().retention_glr_bwd_workspace_size(B, T, D, nseq))
 
 
@@ -766,7 +780,7 @@ def glr_bwd(x, r, i, lam, chunk_states, d_h, c=8.0, cu_seqlens=None, d_state_out
     """
     raw = _ready(stream, x=x, r=r, i=i, lam=lam, chunk_states=chunk_states, d_h=d_h,
                  cu_seqlens=cu_seqlens, d_state_out=d_state_out, workspace=workspace)
-    B, T, D, nseq = _glr_inputs(x, r, i, lam, cu_seqlens)
+    B, T, D, nseq = _glr_inputs("retention_glr_bwd", x, r, i, lam, cu_seqlens)
     states = (nseq or B, D)
     _shaped(d_h, "d_h", x.shape)
     _shaped(chunk_states, "chunk_states", (glr_chunk_slots(B, T, nseq), D), torch.float32)
@@ -799,6 +813,8 @@ def glr_step(x, r, i, lam, state, c=8.0, out_dtype=torch.float32, out=None, stat
     _shaped(state, "state", (N, D), torch.float32)
     _shaped(state_out, "state_out", (N, D), torch.float32)
     _shaped(out, "out", (N, D))
+    if _wide(N | D):
+        raise _too_large("retention_glr_step")
     if out is None:
         out = _new(stream, (N, D), out_dtype, x)
     if state_out is None:
@@ -822,6 +838,8 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out_dtype=None, out=None
     _shaped(weight, "weight", (D,), torch.float32)
     _shaped(bias, "bias", (D,), torch.float32)
     _shaped(out, "out", x.shape, out_dtype)
+    if _wide(ntok | D):
+        raise _too_large("retention_layer_norm_fwd")
     mean = rstd = None
     if out is None:
         out = _new(stream, x.shape, out_dtype or x.dtype, x)
@@ -835,6 +853,8 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out_dtype=None, out=None
 
 
 def layer_norm_bwd_workspace_size(ntok, D):
+    if _wide(ntok | D):
+        return 0
     return int(lib().retention_layer_norm_bwd_workspace_size(ntok, D))
 
 
@@ -852,6 +872,8 @@ def layer_norm_bwd(x, d_y, mean, rstd, weight=None, return_d_affine=True, grad_d
     _shaped(mean, "mean", x.shape[:-1], torch.float32)
     _shaped(rstd, "rstd", x.shape[:-1], torch.float32)
     _shaped(weight, "weight", (D,), torch.float32)
+    if _wide(ntok | D):
+        raise _too_large("retention_layer_norm_bwd")
     dw = db = None
     dx = _new(stream, x.shape, grad_dtype or x.dtype, x)
     if return_d_affine:
@@ -868,6 +890,8 @@ def layer_norm_bwd(x, d_y, mean, rstd, weight=None, return_d_affine=True, grad_d
 
 
 def norm_gate_bwd_workspace_size(ntok, H, dv):
+    if _wide(ntok | H | dv):
+        return 0
     return int(lib().msr_norm_gate_bwd_workspace_size(ntok, H, dv))
 
 
@@ -888,6 +912,8 @@ def norm_gate_bwd(o, g, d_y, weight=None, bias=None, eps=1e-5, return_d_affine=T
     for t, n in ((weight, "weight"), (bias, "bias")):
         if t is not None and (t.dtype != torch.float32 or t.numel() != H * dv):
             raise ValueError(f"{n} must be float32 with H*dv elements")
+    if _wide(ntok | H | dv):
+        raise _too_large("msr_norm_gate_bwd")
     dw = db = None
     gd = grad_dtype or d_y.dtype
     d_o, d_g = _new(stream, o.shape, gd, o), _new(stream, g.shape, gd, g)
