@@ -261,6 +261,8 @@ def abi_version():
 def parallel_workspace_size(dtype, B, T, H, dk, dv):
     """Bytes of workspace the parallel form needs (0: none, the CUDA-core kernel)."""
     code = RET_F32 if dtype == torch.float32 else RET_BF16
+    if _wide(B | T | H | dk | dv):
+        return 0
     return int(lib().retention_parallel_workspace_size(code, B, T, H, dk, dv))
 
 
@@ -274,6 +276,8 @@ def parallel_fwd(q, k, v, gamma, out_dtype=None, out=None, workspace=None, strea
     dv = v.shape[3]
     if k.shape != q.shape or v.shape[:3] != q.shape[:3] or k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k, v shapes/dtypes disagree")
+    if _wide(B | T | H | dk | dv):
+        raise _too_large("retention_parallel_fwd")
     if out is None:
         out = torch.empty(B, T, H, dv, device=q.device, dtype=out_dtype or q.dtype)
     else:
@@ -293,6 +297,8 @@ def parallel_fwd(q, k, v, gamma, out_dtype=None, out=None, workspace=None, strea
 
 def chunkwise_workspace_size(dtype, chunk, B, T, H, dk, dv, nseq=0):
     code = RET_F32 if dtype == torch.float32 else RET_BF16
+    if _wide(chunk | B | T | H | dk | dv | nseq):
+        return 0
     return int(lib().retention_chunkwise_workspace_size(code, chunk, B, T, H, dk, dv, nseq))
 
 
@@ -300,6 +306,8 @@ def chunkwise_executed_chunk(dtype, chunk, dk, dv):
     """The chunk length the chunkwise kernels evaluate for ``chunk`` (0 if
     unsupported); every chunk length gives the same result."""
     code = RET_F32 if dtype == torch.float32 else RET_BF16
+    if _wide(chunk | dk | dv):
+        return 0
     return int(lib().retention_chunkwise_executed_chunk(code, chunk, dk, dv))
 
 
@@ -309,6 +317,8 @@ def alloc_workspace(nbytes, device):
 
 
 def chunkwise_fwd_rope_workspace_size(chunk, B, T, H, dk, dv, nseq=0):
+    if _wide(chunk | B | T | H | dk | dv | nseq):
+        return 0
     return lib().retention_chunkwise_fwd_rope_workspace_size(chunk, B, T, H, dk, dv, nseq)
 
 
@@ -338,6 +348,8 @@ def chunkwise_fwd(q, k, v, gamma, chunk, cu_seqlens=None, state_in=None, return_
         nseq = cu_seqlens.numel() - 1
         if nseq < 1:
             raise ValueError("cu_seqlens needs at least two entries")
+    if _wide(max(int(chunk), 0) | B | T | H | dk | dv | nseq):
+        raise _too_large("retention_chunkwise_fwd")
     nstate = nseq if nseq else B
     if state_in is not None:
         _dev(state_in, "state_in")
@@ -407,6 +419,8 @@ def chunkwise_states(k, v, gamma, chunk, cu_seqlens=None, state_in=None, state_o
     nseq = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
     if cu_seqlens is not None:
         _dev(cu_seqlens, "cu_seqlens")
+    if _wide(max(int(chunk), 0) | B | T | H | dk | dv | nseq):
+        raise _too_large("retention_chunkwise_states")
     need = lib().retention_chunkwise_workspace_size(_dt(k), chunk, B, T, H, dk, dv, nseq)
     if need == 0:
         raise RetentionError(RET_ERR_UNSUPPORTED if _dt(k) == RET_BF16 else RET_ERR_INVALID_ARG,
@@ -433,6 +447,8 @@ def chunkwise_outputs(q, k, v, gamma, chunk, workspace, cu_seqlens=None, has_sta
     B, T, H, dk = q.shape
     dv = v.shape[3]
     nseq = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
+    if _wide(max(int(chunk), 0) | B | T | H | dk | dv | nseq):
+        raise _too_large("retention_chunkwise_outputs")
     if out is None:
         out = torch.empty(B, T, H, dv, device=q.device, dtype=out_dtype or q.dtype)
     ng = None
@@ -461,6 +477,8 @@ def chunkwise_fwd_static_ws(q, k, v, gamma, chunk, cu_seqlens=None, state_in=Non
     B, T, H, dk = q.shape
     dv = v.shape[3]
     nseq = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
+    if _wide(max(int(chunk), 0) | B | T | H | dk | dv | nseq):
+        raise _too_large("retention_chunkwise_fwd_static_ws")
     if out is None:
         out = torch.empty(B, T, H, dv, device=q.device, dtype=out_dtype or q.dtype)
     ng = None
@@ -478,6 +496,8 @@ def chunkwise_fwd_static_ws(q, k, v, gamma, chunk, cu_seqlens=None, state_in=Non
 
 def chunkwise_bwd_workspace_size(dtype, chunk, B, T, H, dk, dv, nseq=0):
     code = RET_F32 if dtype == torch.float32 else RET_BF16
+    if _wide(chunk | B | T | H | dk | dv | nseq):
+        return 0
     return int(lib().retention_chunkwise_bwd_workspace_size(code, chunk, B, T, H, dk, dv, nseq))
 
 
@@ -504,6 +524,8 @@ def chunkwise_bwd(q, k, v, d_out, gamma, chunk, cu_seqlens=None, state_in=None,
         if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must be a 1-D int32 tensor with at least two entries")
         nseq = cu_seqlens.numel() - 1
+    if _wide(max(int(chunk), 0) | B | T | H | dk | dv | nseq):
+        raise _too_large("retention_chunkwise_bwd")
     nstate = nseq if nseq else B
     for t, n in ((state_in, "state_in"), (d_state_out, "d_state_out")):
         if t is not None:
@@ -545,6 +567,8 @@ def rope(q, k, base=10000.0, cu_seqlens=None, q_out=None, k_out=None, stream=Non
         if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must be a 1-D int32 tensor with at least two entries")
         nseq = cu_seqlens.numel() - 1
+    if _wide(B | T | H | d | nseq):
+        raise _too_large("retention_rope")
     q_out = torch.empty_like(q) if q_out is None else q_out
     k_out = torch.empty_like(k) if k_out is None else k_out
     for t, n in ((q_out, "q_out"), (k_out, "k_out")):
@@ -574,6 +598,8 @@ def rla_fwd(q, k, v, window, cu_seqlens=None, out_dtype=None, out=None, workspac
         if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must be a 1-D int32 tensor with at least two entries")
         nseq = cu_seqlens.numel() - 1
+    if _wide(max(int(window), 0) | B | T | H | dk | dv | nseq):
+        raise _too_large("retention_rla_fwd")
     if out is None:
         out = torch.empty(B, T, H, dv, device=q.device, dtype=out_dtype or q.dtype)
     _dev(out, "out")
@@ -598,6 +624,8 @@ def recurrent_step(q, k, v, gamma, state, out_dtype=torch.float32, out=None, str
     dv = v.shape[2]
     if state.dtype != torch.float32 or tuple(state.shape) != (N, H, dk, dv):
         raise ValueError(f"state must be float32 [{N},{H},{dk},{dv}]")
+    if _wide(N | H | dk | dv):
+        raise _too_large("retention_recurrent_step")
     if out is None:
         out = torch.empty(N, H, dv, device=q.device, dtype=out_dtype)
     st = lib().retention_recurrent_step(_ptr(q), _ptr(k), _ptr(v), _dt(q), _gammas(gamma, H),
@@ -619,6 +647,8 @@ def recurrent_steps(q, k, v, gamma, state, out_dtype=torch.float32, out=None, st
     dv = v.shape[3]
     if state.dtype != torch.float32 or tuple(state.shape) != (N, H, dk, dv):
         raise ValueError(f"state must be float32 [{N},{H},{dk},{dv}]")
+    if _wide(N | Tn | H | dk | dv):
+        raise _too_large("retention_recurrent_steps")
     if out is None:
         out = torch.empty(N, Tn, H, dv, device=q.device, dtype=out_dtype)
     else:
@@ -639,6 +669,8 @@ def norm_gate(o, g, weight=None, bias=None, eps=1e-5, out_dtype=None, out=None, 
     ntok = o.numel() // (H * dv)
     if g.numel() != o.numel():
         raise ValueError("g must have as many elements as o")
+    if _wide(ntok | H | dv):
+        raise _too_large("msr_norm_gate")
     if out is None:
         y = torch.empty(o.shape, device=o.device, dtype=out_dtype or o.dtype)
     else:

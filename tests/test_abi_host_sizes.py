@@ -42,7 +42,7 @@ class _Recorder:
         self.calls = []
 
     def __getattr__(self, name):
-        return lambda *args: self.calls.append(name) or 0
+        return lambda *args: self.calls.append(name) or (256 if name.endswith("size") else 0)
 
 
 def _meta(*shape, dtype=torch.bfloat16):
@@ -86,3 +86,58 @@ NEW_CALLS = {
 @pytest.mark.parametrize("name", NEW_CALLS)
 def test_calls_refuse_more_rows_than_a_c_int_holds(monkeypatch, name):
     _check_call(monkeypatch, NEW_CALLS[name], 4)
+
+
+def _gam(h):
+    return [0.5] * h
+
+
+def _qkv(n, axis, dtype=torch.bfloat16):
+    shape = [n if axis == k else 1 for k in range(3)] + [2]
+    return [_meta(*shape, dtype=dtype) for _ in range(3)]
+
+
+OLDER_CALLS = {
+    "parallel_fwd": lambda ops, n: ops.parallel_fwd(*_qkv(n, 1), _gam(1)),
+    "chunkwise_fwd": lambda ops, n: ops.chunkwise_fwd(*_qkv(n, 0), _gam(1), 128),
+    "chunkwise_fwd_chunk": lambda ops, n: ops.chunkwise_fwd(*_qkv(4, 1), _gam(1), n),
+    "chunkwise_states": lambda ops, n: ops.chunkwise_states(*_qkv(n, 1)[:2], _gam(1), 128),
+    "chunkwise_outputs": lambda ops, n: ops.chunkwise_outputs(*_qkv(n, 1), _gam(1), 128, _meta(256)),
+    "chunkwise_fwd_static_ws": lambda ops, n: ops.chunkwise_fwd_static_ws(*_qkv(n, 1), _gam(1), 128),
+    "chunkwise_bwd": lambda ops, n: ops.chunkwise_bwd(*_qkv(n, 1), _qkv(n, 1)[0], _gam(1), 128),
+    "rope": lambda ops, n: ops.rope(*_qkv(n, 1)[:2]),
+    "rla_fwd": lambda ops, n: ops.rla_fwd(*_qkv(n, 1), 8),
+    "recurrent_step": lambda ops, n: ops.recurrent_step(
+        *[_meta(n, 1, 2)] * 3, _gam(1), _meta(n, 1, 2, 2, dtype=torch.float32)),
+    "recurrent_steps": lambda ops, n: ops.recurrent_steps(
+        *[_meta(n, 1, 1, 2)] * 3, _gam(1), _meta(n, 1, 2, 2, dtype=torch.float32)),
+    "norm_gate": lambda ops, n: ops.norm_gate(_meta(n, 1, 2), _meta(n, 2)),
+}
+
+
+@pytest.mark.parametrize("name", OLDER_CALLS)
+def test_retention_calls_refuse_more_rows_than_a_c_int_holds(monkeypatch, name):
+    ops, _ = _lib()
+    monkeypatch.setattr(ops, "_dev", lambda t, name: t)
+    monkeypatch.setattr(ops, "_stream", lambda stream: None)
+    _check_call(monkeypatch, OLDER_CALLS[name], 4)
+
+
+def test_retention_size_queries_refuse_what_a_c_int_does_not_hold():
+    ops, _ = _lib()
+    bf = torch.bfloat16
+    sizes = [4, 128, 2, 128, 128]
+    assert ops.parallel_workspace_size(bf, *sizes) > 0
+    for query in (ops.chunkwise_workspace_size, ops.chunkwise_bwd_workspace_size):
+        assert query(bf, 128, *sizes) > 0
+    assert ops.chunkwise_fwd_rope_workspace_size(128, *sizes) > 0
+    assert ops.chunkwise_executed_chunk(bf, 128, 128, 128) > 0
+    low = 1 << 32
+    for k in range(5):
+        wide = [v + low if j == k else v for j, v in enumerate(sizes)]
+        assert ops.parallel_workspace_size(bf, *wide) == 0
+        assert ops.chunkwise_workspace_size(bf, 128, *wide) == 0
+        assert ops.chunkwise_bwd_workspace_size(bf, 128, *wide) == 0
+        assert ops.chunkwise_fwd_rope_workspace_size(128, *wide) == 0
+    assert ops.chunkwise_workspace_size(bf, 128 + low, *sizes) == 0
+    assert ops.chunkwise_executed_chunk(bf, 128 + low, 128, 128) == 0
