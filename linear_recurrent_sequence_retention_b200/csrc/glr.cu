@@ -1037,22 +1037,25 @@ bool direct(const SeqLayout& L) {
   return L.Ttot <= (L.T > 0 ? 32ll : 16ll) * L.nseq;
 }
 
-// Fills the common arguments and launches `kern` on clusters of `split` CTAs.
+// Launches `kern` on clusters of `split` CTAs, with `bytes` of shared memory and what the exchange
+// takes (exchange_bytes of `warps` warps).  The kernel's limit belongs to the process, and other host
+// threads launch between a call's setting and its launch: so every call sets the same one, that of
+// the largest cluster.
 template <typename... P, typename... A>
-cudaError_t launch_split(void (*kern)(P...), int threads, size_t smem, long long blocks, int split,
+cudaError_t launch_split(void (*kern)(P...), int warps, size_t bytes, long long blocks, int split,
                          cudaStream_t s, A... args) {
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+                                       static_cast<int>(exchange_bytes(kMaxSplit, warps) + bytes));
   if (e == cudaSuccess && split > 8)
     e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(warps * 32);
+  cfg.dynamicSmemBytes = exchange_bytes(split, warps) + bytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1098,11 +1101,9 @@ cudaError_t launch_glr_fwd(const void* x, const void* r, const void* i, DType in
         using Ti = decltype(ti);
         using Th = decltype(th);
         constexpr int M = decltype(mode)::value;
-        const size_t smem = exchange_bytes(p.split, kFwdWarps) +
-                            stages<Ti>() * 3 * kFwdWarps * run_bytes<Ti, M, kFwdRun>();
-        return launch_split(glr_fwd_kernel<Ti, Th, M>, kFwdWarps * 32, smem, blocks, p.split, s,
-                            p, state_in,
-                            state_out, static_cast<Th*>(h), chunk_states);
+        const size_t rows = stages<Ti>() * 3 * kFwdWarps * run_bytes<Ti, M, kFwdRun>();
+        return launch_split(glr_fwd_kernel<Ti, Th, M>, kFwdWarps, rows, blocks, p.split, s, p,
+                            state_in, state_out, static_cast<Th*>(h), chunk_states);
       });
     });
   });
@@ -1142,13 +1143,11 @@ cudaError_t launch_glr_bwd(const void* x, const void* r, const void* i, DType in
           using Tu = decltype(tu);
           using Tg = decltype(tg);
           constexpr int M = decltype(mode)::value;
-          const size_t smem =
-              exchange_bytes(p.split, kBwdWarps) + 2 * kBwdWarps * 32 * sizeof(F2) +
-              stages<Ti>() * kBwdWarps *
-                  (3 * run_bytes<Ti, M, kBwdRun>() + run_bytes<Tu, M, kBwdRun>());
-          return launch_split(glr_bwd_kernel<Ti, Tu, Tg, M>, kBwdWarps * 32, smem, blocks,
-                              p.split, s, p,
-                              chunk_states, static_cast<const Tu*>(d_h), d_state_out,
+          const size_t rows = stages<Ti>() * kBwdWarps *
+                              (3 * run_bytes<Ti, M, kBwdRun>() + run_bytes<Tu, M, kBwdRun>());
+          const size_t states = 2 * kBwdWarps * 32 * sizeof(F2);
+          return launch_split(glr_bwd_kernel<Ti, Tu, Tg, M>, kBwdWarps, states + rows, blocks,
+                              p.split, s, p, chunk_states, static_cast<const Tu*>(d_h), d_state_out,
                               static_cast<Tg*>(dx), static_cast<Tg*>(dr), static_cast<Tg*>(di),
                               d_state_in, partial);
         });
