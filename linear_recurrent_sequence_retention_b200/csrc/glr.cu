@@ -366,12 +366,16 @@ __device__ __forceinline__ float4 pack(const Map& m) {
 // bytes.  A buffer is written again two rounds later; by then every reader has
 // passed the block barrier (warp maps) of the round between, and a CTA sends its
 // next map only after that, so a map received tells that the sender's warps have
-// read everything of the round before last.
-struct Exchange {
+// read everything of the round before last.  The maps and rows behind it start on 128-byte lines
+// (16 bytes off 32, the forward of 2 x 8192 x 4096 took 0.152 ms instead of 0.135 ms).
+struct alignas(128) Exchange {
   uint64_t bar[2];
-  int abort;
+  int abort;                            // a wait of this CTA has given up
   int seq;                              // of longest_first
-  int pad[2];
+  int sent;                             // rounds whose map this CTA has sent
+  int failed;                           // a wait of any CTA has given up (set by it at the end)
+  int all_sent[kMaxSplit];              // `sent` of every CTA, where one has failed
+  int stop;                             // `abort` as the sending warp saw it before the round's barrier
 };
 __host__ __device__ constexpr size_t exchange_bytes(int split, int warps) {
   return sizeof(Exchange) + 2 * (warps + (split > 1 ? split : 0)) * sizeof(Maps);
@@ -416,42 +420,84 @@ __device__ __forceinline__ int longest_first(const SeqLayout& L, int slot, Excha
   return ex.seq;
 }
 
-// Start of a kernel: every CTA of the cluster is running and its barriers are set up
-// before any map is sent.
-__device__ __forceinline__ void exchange_begin(Exchange& ex, int S) {
+// Start of a kernel, before anything is on its way: the fence makes these writes come before
+// those that other CTAs make later.
+__device__ __forceinline__ void exchange_init(Exchange& ex, int S) {
+  if (S == 1 || threadIdx.x != 0) return;
+  tc::mbar_init(&ex.bar[0], 1);
+  tc::mbar_init(&ex.bar[1], 1);
+  ex.abort = ex.sent = ex.failed = 0;
+  tc::fence_barrier_init();
+  tc::fence_cluster();
+}
+// Before the first map is sent: every CTA of the cluster is running and its barriers are set up.
+__device__ __forceinline__ void exchange_begin(int S) {
   if (S == 1) return;
-  if (threadIdx.x == 0) {
-    tc::mbar_init(&ex.bar[0], 1);
-    tc::mbar_init(&ex.bar[1], 1);
-    ex.abort = 0;
-    tc::fence_barrier_init();
-  }
   __syncthreads();
   tc::cluster_arrive_relaxed();
   tc::cluster_wait();
 }
-// End of a kernel: no CTA leaves while maps may still be on their way to it.
-__device__ __forceinline__ void exchange_end(int S) {
-  if (S == 1) return;
-  tc::cluster_arrive_relaxed();
-  tc::cluster_wait();
+__device__ __forceinline__ bool gave_up(const Exchange& ex) {
+  return *static_cast<const volatile int*>(&ex.abort) != 0;
 }
-// One warp sends its CTA's map of round `n` to every CTA of the cluster.  The stores carry
-// their own completion, so nothing here waits for stores to global memory (the release
-// of a cluster barrier would: 0.38 ms instead of 0.27 ms at 2 x 8192 x 4096, forward).
-__device__ __forceinline__ void send(Exchange& ex, Maps* cta, const Map& mine, int n, int S,
-                                     int rank, int lane) {
+__device__ __forceinline__ void send_map(Exchange& ex, Maps* cta, const Map& mine, int n, int S,
+                                         int rank, int lane) {
   Maps* to = cta + (n & 1) * S;
   uint64_t* bar = &ex.bar[n & 1];
-  if (lane == 0 && !*static_cast<volatile int*>(&ex.abort))
-    tc::mbar_arrive_expect_tx(bar, S * sizeof(Maps));
+  if (lane == 0) tc::mbar_arrive_expect_tx(bar, S * sizeof(Maps));
   for (int q = 0; q < S; ++q)
     st_async_f32x4(tc::cluster_addr(&to[rank][lane], q), pack(mine), tc::cluster_addr(bar, q));
+}
+// Before the block barrier of a round, by the warp that will send: all its lanes then read the same
+// (a vote in `send` cost the gradients 64 bytes of spills).
+__device__ __forceinline__ void send_or_stop(Exchange& ex, int S, int lane) {
+  if (S > 1 && lane == 0) ex.stop = gave_up(ex);
+}
+// One warp sends its CTA's map of round `n` to every CTA of the cluster, unless a wait of this
+// CTA has given up: so it has received every map of round n - 1, and no CTA is ever more than one
+// round ahead of another.  The stores carry their own completion, so nothing here waits for
+// stores to global memory (the release of a cluster barrier would: 0.38 ms instead of 0.27 ms at
+// 2 x 8192 x 4096, forward).
+__device__ __forceinline__ void send(Exchange& ex, Maps* cta, const Map& mine, int n, int S,
+                                     int rank, int lane) {
+  if (*static_cast<const volatile int*>(&ex.stop)) return;
+  if (lane == 0) ex.sent = n + 1;
+  send_map(ex, cta, mine, n, S, rank, lane);
 }
 // Waits for the maps of round `n`.  The wait is bounded; once one has run out the others
 // return at once, the rounds go on without exchange and the error is reported.
 __device__ __forceinline__ void receive(Exchange& ex, int n, unsigned* err) {
+  if (gave_up(ex)) return;
   tc::mbar_wait_cluster(&ex.bar[n & 1], (n >> 1) & 1, &ex.abort, err);
+}
+// End of a kernel: no CTA leaves while maps may still be on their way to it.  Where no wait has
+// given up, each CTA has received every map of every round.  Otherwise a CTA that gave up tells
+// all of them; all tell each other how many rounds they have sent, those that are behind by the one
+// round send it as well (its contents count for nothing), and each waits, bounded again, for
+// the last two rounds, before which everything has arrived.
+__device__ __forceinline__ void exchange_end(Exchange& ex, Maps* cta, int S, int rank) {
+  if (S == 1) return;
+  const int t = threadIdx.x;
+  __syncthreads();                        // abort and sent are final
+  if (t < S && ex.abort) {
+    tc::st_cluster_s32(tc::cluster_addr(&ex.failed, t), 1);
+    tc::fence_cluster();
+  }
+  tc::cluster_arrive_relaxed();
+  tc::cluster_wait();
+  if (!*static_cast<volatile int*>(&ex.failed)) return;
+  if (t < S) {
+    tc::st_cluster_s32(tc::cluster_addr(&ex.all_sent[rank], t), ex.sent);
+    tc::fence_cluster();
+  }
+  tc::cluster_arrive_relaxed();
+  tc::cluster_wait();
+  const volatile int* all = ex.all_sent;
+  int most = 0;
+  for (int q = 0; q < S; ++q) most = max(most, all[q]);
+  if (t < 32 && all[rank] < most) send_map(ex, cta, identity(), most - 1, S, rank, t);
+  for (int n = max(most - 2, 0); n < most; ++n)
+    tc::mbar_wait_drain(&ex.bar[n & 1], (n >> 1) & 1);
 }
 
 // ---- forward ---------------------------------------------------------------
@@ -460,12 +506,13 @@ template <typename Ti, typename Th, int MODE>
 __global__ void __launch_bounds__(kFwdWarps * 32, 4)
 glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ state_out,
                Th* __restrict__ h, float* __restrict__ chunk_states) {
-  extern __shared__ __align__(16) char smem[];
+  extern __shared__ __align__(128) char smem[];
   constexpr int kWarps = kFwdWarps, kRun = kFwdRun;
   constexpr int kArray = run_bytes<Ti, MODE, kRun>(), kStages = stages<Ti>();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int S = p.split, rank = static_cast<int>(blockIdx.x % S);
   Exchange& ex = *reinterpret_cast<Exchange*>(smem);
+  exchange_init(ex, S);
   Maps(*warp_maps)[kWarps] = reinterpret_cast<Maps(*)[kWarps]>(smem + sizeof(Exchange));   // [2]
   Maps* cta_maps = reinterpret_cast<Maps*>(warp_maps + 2);                // [2][S]
   char* ring = smem + exchange_bytes(S, kWarps) + warp * (kStages * 3 * kArray);
@@ -510,7 +557,7 @@ glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ s
   const F2 lm = load2(p.lam, 0, cA, cB, D);
   const F2 ysc = gate_scale(p.c, lm);
   F2 carry = load2(state_in, static_cast<size_t>(seq) * D, cA, cB, D);
-  exchange_begin(ex, S);
+  exchange_begin(S);
   const auto run = [&](auto small) {
     for (int j = 0; j < rounds; ++j) {
       if (kStages > 1) fetch(j + 1);
@@ -534,6 +581,7 @@ glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ s
       if (kStages == 1) fetch(j + 1);
       Maps* wm = warp_maps[j & 1];
       wm[warp][lane] = pack(m);
+      if (warp == kWarps - 1) send_or_stop(ex, S, lane);
       __syncthreads();
       F2 enter, hs;                       // the states that enter the tile and the warp's run
       if (S == 1) {
@@ -585,7 +633,7 @@ glr_fwd_kernel(Args p, const float* __restrict__ state_in, float* __restrict__ s
     run(std::false_type{});
   if (state_out && rank == 0 && warp == 0)
     store2(state_out, static_cast<size_t>(seq) * D, carry, cA, cB, D);
-  exchange_end(S);
+  exchange_end(ex, cta_maps, S, rank);
 }
 
 // ---- gradients -------------------------------------------------------------
@@ -609,7 +657,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2)
 glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restrict__ dh,
                const float* __restrict__ d_state_out, Tg* __restrict__ dx, Tg* __restrict__ dr,
                Tg* __restrict__ di, float* __restrict__ d_state_in, float* __restrict__ partial) {
-  extern __shared__ __align__(16) char smem[];
+  extern __shared__ __align__(128) char smem[];
   using P = Pairs<sizeof(Ti) == 2 && MODE != kOdd>;
   constexpr int kWarps = kBwdWarps, kRun = kBwdRun;
   constexpr int kArray = run_bytes<Ti, MODE, kRun>(), kUp = run_bytes<Tu, MODE, kRun>();
@@ -617,6 +665,7 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int S = p.split, rank = static_cast<int>(blockIdx.x % S);
   Exchange& ex = *reinterpret_cast<Exchange*>(smem);
+  exchange_init(ex, S);
   Maps(*warp_maps)[kWarps] = reinterpret_cast<Maps(*)[kWarps]>(smem + sizeof(Exchange));   // [2]
   Maps* cta_maps = reinterpret_cast<Maps*>(warp_maps + 2);                // [2][S]
   F2(*wf)[kWarps][32] = reinterpret_cast<F2(*)[kWarps][32]>(smem + exchange_bytes(S, kWarps));
@@ -661,7 +710,7 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
   const size_t so = static_cast<size_t>(seq) * D;
   F2 carry = load2(d_state_out, so, cA, cB, D);
   F2 usum = f2(0.f);
-  exchange_begin(ex, S);
+  exchange_begin(S);
   const auto run = [&](auto small) {
     for (int j = rounds - 1; j >= 0; --j) {
       const int n = rounds - 1 - j;
@@ -692,6 +741,7 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
       Maps* wm = warp_maps[n & 1];
       wm[warp][lane] = pack(Map{fw.A, w});
       wf[n & 1][warp][lane] = fw.V;
+      if (warp == 0) send_or_stop(ex, S, lane);
       __syncthreads();
       F2 hs = cs, e;                      // the state and the gradient that enter the run
 #pragma unroll 1
@@ -764,7 +814,7 @@ glr_bwd_kernel(Args p, const float* __restrict__ chunk_states, const Tu* __restr
     for (int q = 1; q < kWarps; ++q) usum = P::add(usum, wf[0][q][lane]);
     store2(partial, (static_cast<size_t>(seq) * S + rank) * D, usum, cA, cB, D);
   }
-  exchange_end(S);
+  exchange_end(ex, cta_maps, S, rank);
 }
 
 // ---- short sequences ------------------------------------------------------------

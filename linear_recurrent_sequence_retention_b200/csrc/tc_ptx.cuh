@@ -413,6 +413,15 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
 }
 
+__device__ __forceinline__ void st_cluster_s32(uint32_t remote, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
+}
+// Orders this thread's accesses before those that follow it (cluster scope); with a relaxed
+// barrier arrival after it, before what other CTAs do past the barrier.
+__device__ __forceinline__ void fence_cluster() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+
 // Reads a float from the same shared-memory offset in CTA `rank` of the cluster.
 __device__ __forceinline__ float ld_cluster_f32(const void* local, uint32_t rank) {
   uint32_t remote;
