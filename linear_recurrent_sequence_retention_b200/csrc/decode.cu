@@ -107,10 +107,10 @@ decode_step_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k,
 template <typename Tin, typename To, int VEC>
 cudaError_t decode_typed(const void* q, const void* k, const void* v, float* state, void* o,
                          int N, int H, int dk, int dv, const HeadDecay& dec, cudaStream_t s) {
-  size_t smem = sizeof(float) * (2 * dk + kWarps * 32 * VEC);
+  const auto bytes = [](int d) { return sizeof(float) * (2 * d + kWarps * 32 * VEC); };
+  const size_t smem = bytes(dk);
   auto kern = decode_step_kernel<Tin, To, VEC>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  cudaError_t e = limit_smem(kern, bytes(1024));          // d_k <= 1024
   if (e != cudaSuccess) return e;
   dim3 grid((dv + 32 * VEC - 1) / (32 * VEC), H, N);
   kern<<<grid, kWarps * 32, smem, s>>>(static_cast<const Tin*>(q), static_cast<const Tin*>(k),
@@ -274,10 +274,12 @@ template <typename Tin, typename To, int MAXT>
 cudaError_t decode_multi_typed(const void* q, const void* k, const void* v, float* state,
                                void* o, int N, int Tn, int H, int dk, int dv,
                                const HeadDecay& dec, cudaStream_t s) {
-  const size_t smem = sizeof(float) * (2 * MAXT * dk + MAXT * kMultiCols + MAXT * MAXT);
+  const auto bytes = [](int d) {
+    return sizeof(float) * (2 * MAXT * d + MAXT * kMultiCols + MAXT * MAXT);
+  };
+  const size_t smem = bytes(dk);
   auto kern = decode_multi_kernel<Tin, To, MAXT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  cudaError_t e = limit_smem(kern, bytes(512));           // d_k <= 512
   if (e != cudaSuccess) return e;
   dim3 grid((dv + kMultiCols - 1) / kMultiCols, H, N);
   kern<<<grid, kWarps * 32, smem, s>>>(static_cast<const Tin*>(q), static_cast<const Tin*>(k),

@@ -556,9 +556,10 @@ PFN_cuTensorMapEncodeTiled_v12000 dt_encode_fn() {
 
 }  // namespace
 
+constexpr uint32_t kDtSmemLimit = 232448;     // shared memory a block can have
 bool decode_steps_tc_supported(int Tn, int dk, int dv) {
   return Tn >= 1 && Tn <= kDtMaxT && (dk == 128 || dk == 256) && dv % 128 == 0 &&
-         DtLayout(dk, dv).smem <= 232448 &&
+         DtLayout(dk, dv).smem <= kDtSmemLimit &&
          static_cast<uint32_t>(Tn * (2 * dk + dv) * 2) <= kDtStage;
 }
 
@@ -621,8 +622,7 @@ cudaError_t launch_decode_steps_tc(const void* q, const void* k, const void* v, 
   p.dec = dec;
   p.err = err;
   const size_t smem = DtLayout(dk, dv).smem;
-  cudaError_t e = cudaFuncSetAttribute(decode_multi_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  cudaError_t e = limit_smem(decode_multi_tc_kernel, kDtSmemLimit);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
   e = cudaGetDevice(&dev);

@@ -29,6 +29,15 @@ struct ChunkWorkspace {
 
 size_t chunkwise_meta_bytes(int nseq);
 
+// Lets `kern` use up to `most` bytes of dynamic shared memory.  The limit belongs to the process and
+// other host threads launch between this and the caller's launch, so `most` is the same at every call:
+// what the largest supported sizes take.
+template <typename K>
+cudaError_t limit_smem(K* kern, size_t most) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(most));
+}
+
 // CUDA-core (fp32 FFMA) kernels.
 cudaError_t launch_parallel_simt(const void* q, const void* k, const void* v, DType in_t,
                                  void* o, DType o_t, int B, int T, int H, int dk, int dv,

@@ -579,15 +579,28 @@ chunk_grad_simt_kernel(const Tin* __restrict__ a, const Tin* __restrict__ b,
   }
 }
 
+// Dynamic shared memory of each kernel; d_k and d_v are at most kMaxDim.
+constexpr int kMaxDim = 256;
+constexpr size_t state_smem(int dk) { return sizeof(float) * (kStateTok * dk + kStateTok * 32); }
+constexpr size_t grad_smem(int da, int dc, bool trans) {
+  return sizeof(float) * ((kRows + kKeys) * (da + 1) + kKeys * dc + kRows * (kKeys + 1) +
+                          (trans ? 32 * (dc + 1) : 0));
+}
+constexpr size_t parallel_smem(int dk, int dv) {
+  return sizeof(float) * (2 * kRows * (dk + 1) + kKeys * dv + kRows * (kKeys + 1));
+}
+constexpr size_t out_smem(int dk, int dv) {
+  return parallel_smem(dk, dv) + sizeof(float) * kRows * 8;
+}
+
 template <typename Tin>
 cudaError_t launch_state_pass(bool rev, const void* k, const void* v, const SeqLayout& L,
                               const int32_t* chunk_base, const float* state_in, float* state_out,
                               float* states, int H, int dk, int dv, const HeadDecay& dec,
                               cudaStream_t s) {
-  const size_t smem = sizeof(float) * (kStateTok * dk + kStateTok * 32);
+  const size_t smem = state_smem(dk);
   auto kern = rev ? chunk_state_simt_kernel<Tin, true> : chunk_state_simt_kernel<Tin, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  cudaError_t e = limit_smem(kern, state_smem(kMaxDim));
   if (e != cudaSuccess) return e;
   dim3 grid((dv + 31) / 32, H, L.nseq);
   kern<<<grid, kThreads, smem, s>>>(static_cast<const Tin*>(k), static_cast<const Tin*>(v), L,
@@ -599,12 +612,9 @@ template <typename Tin, bool kAnti, bool kTrans>
 cudaError_t launch_grad_pass(const void* a, const void* b, const void* c, const SeqLayout& L,
                              const int32_t* chunk_base, const float* states, float* out, int H,
                              int da, int dc, const HeadDecay& dec, cudaStream_t s) {
-  const size_t smem =
-      sizeof(float) * ((kRows + kKeys) * (da + 1) + kKeys * dc + kRows * (kKeys + 1) +
-                       (kTrans ? 32 * (dc + 1) : 0));
+  const size_t smem = grad_smem(da, dc, kTrans);
   auto kern = chunk_grad_simt_kernel<Tin, kAnti, kTrans>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  cudaError_t e = limit_smem(kern, grad_smem(kMaxDim, kMaxDim, kTrans));
   if (e != cudaSuccess) return e;
   dim3 grid((L.Ttot + kRows - 1) / kRows, H);
   kern<<<grid, kThreads, smem, s>>>(static_cast<const Tin*>(a), static_cast<const Tin*>(b),
@@ -643,10 +653,9 @@ cudaError_t chunkwise_bwd_typed(const void* q, const void* k, const void* v, con
 template <typename Tin, typename To>
 cudaError_t parallel_typed(const void* q, const void* k, const void* v, void* o, int B, int T,
                            int H, int dk, int dv, const HeadDecay& dec, cudaStream_t s) {
-  size_t smem = sizeof(float) * (2 * kRows * (dk + 1) + kKeys * dv + kRows * (kKeys + 1));
+  const size_t smem = parallel_smem(dk, dv);
   auto kern = parallel_simt_kernel<Tin, To>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  cudaError_t e = limit_smem(kern, parallel_smem(kMaxDim, kMaxDim));
   if (e != cudaSuccess) return e;
   dim3 grid((T + kRows - 1) / kRows, H, B);
   kern<<<grid, kThreads, smem, s>>>(static_cast<const Tin*>(q), static_cast<const Tin*>(k),
@@ -663,10 +672,9 @@ cudaError_t chunkwise_typed(int phases, const void* q, const void* k, const void
                             ChunkWorkspace ws, int H, int dk, int dv, const HeadDecay& dec,
                             cudaStream_t s) {
   if (phases & 1) {
-    size_t smem = sizeof(float) * (kStateTok * dk + kStateTok * 32);
+    const size_t smem = state_smem(dk);
     auto kern = chunk_state_simt_kernel<Tin, false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    cudaError_t e = limit_smem(kern, state_smem(kMaxDim));
     if (e != cudaSuccess) return e;
     dim3 grid((dv + 31) / 32, H, L.nseq);
     kern<<<grid, kThreads, smem, s>>>(static_cast<const Tin*>(k), static_cast<const Tin*>(v), L,
@@ -676,11 +684,9 @@ cudaError_t chunkwise_typed(int phases, const void* q, const void* k, const void
     if (e != cudaSuccess) return e;
   }
   if (L.Ttot == 0 || !(phases & 2)) return cudaSuccess;
-  size_t smem = sizeof(float) * (2 * kRows * (dk + 1) + kKeys * dv + kRows * (kKeys + 1) +
-                                 kRows * 8);
+  const size_t smem = out_smem(dk, dv);
   auto kern = chunk_out_simt_kernel<Tin, To, Tg>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  cudaError_t e = limit_smem(kern, out_smem(kMaxDim, kMaxDim));
   if (e != cudaSuccess) return e;
   dim3 grid((L.Ttot + kRows - 1) / kRows, H);
   kern<<<grid, kThreads, smem, s>>>(static_cast<const Tin*>(q), static_cast<const Tin*>(k),
