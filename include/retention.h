@@ -496,10 +496,13 @@ RET_API ret_status msr_norm_gate(const void* o, ret_dtype o_dtype, const ret_nor
 /*
  * Gated linear recurrence (ql.gl blog on Griffin/Hawk, section "Hawk":
  * h_t = a_t . h_(t-1) + b_t . x_t element by element, the gates computed from
- * the token).  The page gives no formula for the gates; the form taken is a
- * decay that depends on the token through a sigmoid and an input gate scaled so
- * that the state keeps unit variance.  For each channel, with the projected
- * gate inputs r_t, i_t and a learned parameter lam:
+ * the token).  The page gives no formula for the gates; the form taken is that
+ * of the paper behind it (De et al. 2024, "Griffin: Mixing Gated Linear
+ * Recurrences with Local Attention for Efficient Language Models", its real-gated
+ * linear recurrent unit, with the constant c = 8): a decay that depends on the
+ * token through a sigmoid and an input gate scaled so that the state keeps unit
+ * variance.  For each channel, with the projected gate inputs r_t, i_t and a
+ * learned parameter lam:
  *     s_t = sigmoid(r_t),  y_t = c softplus(lam) s_t,  a_t = exp(-y_t)
  *     b_t = sqrt(1 - a_t^2) sigmoid(i_t)
  *     h_t = a_t h_(t-1) + b_t x_t

@@ -16,12 +16,12 @@
 // enters each 64-token tile, which the forward stored.  The inputs of the next
 // round are copied to shared memory (cp.async) while the current one is computed.
 //
-// Measured at 2 x 8192 x 4096 bf16: forward 0.140 ms for 0.54 GB (59 % of the measured
-// copy rate), gradients 0.268 ms for 0.94 GB (54 %).  Neither HBM nor a pipe is full
-// (special functions 55 %, issue 50 %): a round is a chain of ~2 us (gates, block barrier,
-// exchange, apply) and 128 (sequence, channel group) pairs give each SM only about two CTAs to
-// overlap, unevenly (256 CTAs on 148 SMs).  With 16 sequences of 1024 tokens, the same bytes, no
-// exchange and a full SM, the times are 0.103 ms (80 %) and 0.223 ms (65 %).  Deeper prefetch (3 or
+// Measured at 2 x 8192 x 4096 bf16: forward 0.134 ms for 0.54 GB (61 % of the measured
+// copy rate), gradients 0.266 ms for 0.94 GB (54 %).  Neither HBM nor a pipe is full
+// (special functions 56 %, issue 50 %; gradients 36 % and 65 %): a round is a chain of ~2 us (gates,
+// block barrier, exchange, apply), and with 128 registers and 256 CTAs an SM has fewer than two CTAs
+// to overlap, unevenly (256 on 148).  With 16 sequences of 1024 tokens, the same bytes, no
+// exchange and a full SM, the times are 0.101 ms (82 %) and 0.213 ms (68 %).  Deeper prefetch (3 or
 // 4 stages), 32-channel CTAs, 8 warps of 8 tokens forward, results that leave through shared memory
 // in 16-byte pieces and computing the next round's gates before the exchange is awaited
 // changed the first case by less than 5 %, or made it slower.
@@ -42,9 +42,10 @@ constexpr int kMaxSplit = 16;       // CTAs of a cluster
 constexpr int kFwdWarps = 4, kFwdRun = kTile / kFwdWarps;
 constexpr int kBwdWarps = 8, kBwdRun = kTile / kBwdWarps;
 // Rounds whose rows are in shared memory at once.  Two of float32 would leave room for only one
-// CTA of the gradients on an SM (0.320 ms instead of 0.197 ms at 2 x 8192 x 2048), and two of the
-// forward (0.062 instead of 0.056 ms at 17 sequences, 9001 tokens x 1001; even at 2 x 8192 x 2048).
-// With one the next rows are on their way from the moment these have been read.
+// CTA of the gradients on an SM (0.213 ms instead of 0.185 ms at 2 x 8192 x 2048, 0.106 instead of
+// 0.079 ms at 17 sequences, 9001 tokens x 1001).  The forward gains at these (0.089 instead of 0.093 and
+// 0.049 instead of 0.051 ms) and loses where SMs are full (0.072 instead of 0.063 ms at 64 x 300 x
+// 1001).  With one the next rows are on their way from the moment these have been read.
 template <typename T> constexpr int stages() { return sizeof(T) == 2 ? 2 : 1; }
 
 // How a lane's two channels lie and how rows reach shared memory.
@@ -63,9 +64,9 @@ __device__ __forceinline__ F2 mul(F2 a, F2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ F2 add(F2 a, F2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) { return __ffma2_rn(a, b, c); }
 // The same, or one instruction per channel: the gradients of float32 rows, and of bf16 rows whose
-// channels come apart (kOdd), need fewer registers and are faster so, 0.190 ms instead of 0.197 ms
-// at 2 x 8192 x 2048 float32.  Packed, bf16 takes 0.268 instead of 0.283 ms at 2 x 8192 x 4096, and
-// the forward 0.096 instead of 0.104 ms at 2 x 8192 x 2048 float32.
+// channels come apart (kOdd), need fewer registers and are faster so, 0.185 ms instead of 0.192 ms
+// at 2 x 8192 x 2048 float32.  Packed, bf16 takes 0.266 instead of 0.275 ms at 2 x 8192 x 4096, and
+// the forward there 0.135 instead of 0.150 ms (float32 at 2 x 8192 x 2048 0.093 instead of 0.094).
 template <bool PACKED> struct Pairs {
   static __device__ __forceinline__ F2 mul(F2 a, F2 b) {
     if constexpr (PACKED) return __fmul2_rn(a, b);
@@ -132,7 +133,10 @@ __device__ __forceinline__ F2 gate_scale(float c, F2 lam) {
 // 1 - a = 1 - 2^-n + 2^-n w, so 1 - a^2 = (1 - a)(1 + a) cancels nothing for decays
 // near one.  From n = 127 on (y above 87.7, a below 8e-39) 2^-n is taken as zero,
 // and root is zero where 1 - a^2 is below the normal range.
-// SMALL: y is known to be at most kSmall, so n = 0: the same bits from half the work.
+// SMALL: y is known to be at most kSmall, so n = 0: the same bits from half the work.  A CTA takes the
+// general form where one of its channels needs it, and in the last group where D is no multiple of
+// 64; all channels in it, 2 x 8192 x 4096 bf16 takes 155 / 284 us forward / gradients instead of
+// 134 / 266, 16 x 1024 x 4096 109 / 228 instead of 101 / 213.
 constexpr float kSmall = 0.3465f;
 template <bool SMALL>
 __device__ __forceinline__ void decay(float y, float& a, float& root) {
@@ -391,8 +395,9 @@ __device__ __forceinline__ void st_async_f32x4(uint32_t remote, float4 v, uint32
 
 // The sequence of a cluster that is the slot-th to start: packed sequences go by length, the longest
 // first (it ends last), where there are at most 128 of them; among more, one weighs less.  Every
-// cluster ranks them for itself.  17 sequences of 9001 tokens x 1001 float32, forward / gradients:
-// 42 / 84 us in this order, 53 / 98 in the given one (clusters of four).
+// cluster ranks them for itself.  Forward / gradients in us in this order and in the given one: 17
+// sequences of 9001 tokens x 1001 float32 51 / 79 and 58 / 108, 64 of 200000 x 1024 bf16 351 / 688 and
+// 459 / 889.
 constexpr int kMaxRanked = 128;
 static_assert(kMaxRanked <= kFwdWarps * 32 && kMaxRanked <= kBwdWarps * 32, "a thread each");
 __device__ __forceinline__ int longest_first(const SeqLayout& L, int slot, Exchange& ex,
@@ -990,7 +995,9 @@ __device__ __forceinline__ float sigmoid_over_softplus(float x) {
 }
 
 // d_lam = (sum of the partial rows) sigmoid(lam) / softplus(lam).  32 channels
-// per block; eight row groups, each in order, then the groups in order.
+// per block; eight row groups, each in order, then the groups in order.  There is a row per sequence
+// and CTA of a cluster: with very many short sequences this chain is most of the gradients' time
+// (65536 x 1 x 256: 1.25 ms, the forward 0.16 ms).
 __global__ void __launch_bounds__(256)
 glr_dlam_kernel(const float* __restrict__ partial, const float* __restrict__ lam,
                 float* __restrict__ d_lam, long long rows, int D) {
@@ -1044,13 +1051,15 @@ cudaError_t by_mode(bool any_bf16, int D, F&& f) {
 // has ceil(tiles / S) rounds and about one more to start and end, and finds room the later the
 // larger it is (2 % per CTA, 30 % more where clusters of sixteen share SMs).  Sizes that are not
 // listed are placed badly.  Measured in us, forward / gradients: 2 x 8192 x 4096 bf16 S = 1:
-// 186/309, 2: 142/274, 4: 152/280, 7: 162/332, 16: 178/366; 1 x 16384 x 1024 S = 4: 120/186,
-// 8: 78/146, 12: 61/112, 14: 67/146, 16: 60/130; 1 x 1024 x 2048 S = 1: 26/43, 8: 9/15, 16: 11/20.
+// 178/296, 2: 134/266, 4: 148/271, 7: 158/324, 16: 173/360; 1 x 16384 x 1024 S = 4: 116/187,
+// 8: 72/141, 12: 57/106, 14: 64/144, 16: 57/128; 1 x 1024 x 2048 S = 1: 25/41, 8: 9/15, 16: 11/21.
 // Packed sequences differ in length, which the host does not know: the SMs share the sum, each
 // cluster rounded up and started, while the longest, taken as four times the average, goes on
-// alone (64 sequences, 200000 tokens x 1024: S = 1: 509/832, 2: 362/694, 4: 387/785, 16: 684/1363;
-// 17 of 9001 x 1001 float32 S = 1: 98/169, 3: 50/84, 16: 96/194; 40 of 20000 x 2048 bf16 S = 1:
-// 76/146, 4: 125/234).
+// alone (64 sequences, 200000 tokens x 1024: S = 1: 490/809, 2: 351/688, 4: 378/780, 16: 683/1391;
+// 17 of 9001 x 1001 float32 S = 1: 95/154, 3: 51/79, 4: 44/82, 16: 104/195; 40 of 20000 x 2048 bf16
+// S = 1: 74/140, 2: 82/181, 4: 128/242).  That is about what a uniformly cut batch has.  A batch with
+// one much longer sequence gets too few CTAs for it: 8192 tokens beside 127 single ones at D = 2048
+// take 192/313, alone 45/79; beside 32 at D = 4096 184/305, alone 74/180.
 constexpr double kSms = 148.0;
 int split_of(const SeqLayout& L, int D) {
   const double pairs = static_cast<double>((D + kChan - 1) / kChan) * L.nseq;
@@ -1081,8 +1090,10 @@ int split_of(const SeqLayout& L, int D) {
 
 // Whether threads walk their sequences alone: up to 32 tokens per sequence (16 on average where the
 // lengths differ, which the host does not know).  Measured in us, forward / gradients, alone
-// and by tiles: 256 x 4 x 4096 bf16 15 / 32 and 130 / 253, 32 x 16 x 2048 6.0 / 9.6 and 10.9 / 20.9,
-// 128 x 64 x 4096 77 / 196 and 66 / 163.
+// and by tiles: 256 x 4 x 4096 bf16 15 / 32 and 111 / 233, 32 x 16 x 2048 6.2 / 10 and 10.8 / 20,
+// 128 x 64 x 4096 78 / 196 and 66 / 158.  A packed batch whose average is short because of many short
+// sequences beside a long one loses by it, a thread walking the long one: 4096 tokens beside 300 single
+// ones x 2048 919 / 1641 and 113 / 181 (alone 24 / 44), 1900 beside 127 318 / 539 and 60 / 100.
 bool direct(const SeqLayout& L) {
   return L.Ttot <= (L.T > 0 ? 32ll : 16ll) * L.nseq;
 }

@@ -1,6 +1,9 @@
 // Gradients of the per-head GroupNorm + Swish gate (formulas in include/retention.h).
-// HBM-bound: o, g and d_y are read and d_o, d_g written once.  Measured at 16384 x 16 x 512 bf16:
-// 0.230 ms (5.8 TB/s, 89 % of the measured copy rate); instruction issue is next (over 70 %).
+// Bound by HBM, then by instruction issue (75 %): o, g and d_y are read and d_o, d_g written once.
+// Measured at 16384 x 16 x 512 bf16: 0.232 ms in a few graph replays (5.8 TB/s, 88 % of the measured
+// copy rate), 0.263 ms in a loop of 3000 calls (78 %).  With a float32 o (8192 x 8 x 256, the rest bf16)
+// 0.046 ms, 67 %: 38 us and the sum of the partial gradients, with 69 % of the issue slots used,
+// since every tensor is then copied and stored in 8- or 16-byte vectors of four channels.
 //
 // A (token, head) row belongs to TPR threads (8 to 64, 16 channels each); up to a warp its sums
 // are shuffles alone.  The threads stay with their head and walk the tokens: their channels' sums
